@@ -362,6 +362,187 @@ int pace_prefill_f32(int32_t batch, int32_t heads, int32_t d_k, int32_t d_v, int
                      const float *alpha, const float *beta, float *state, float *out,
                      void *stream);
 
+/* ------------------------------------------------------------------------
+ * The layers beside the gated delta rule.  A hybrid model that decodes its
+ * recurrent states with this library also runs, around them: head norms with
+ * the position rotation in front of every layer, linear-attention layers with
+ * a fixed decay for each head, and softmax layers over a KV cache, held here
+ * in 4 bits like the recurrent states.  These entry points keep no handle: the
+ * caller owns every buffer, nothing is allocated and no call waits, so all of
+ * them can be captured into a graph.  Calls that may run at the same time
+ * must not share a workspace.
+ * ------------------------------------------------------------------------ */
+
+/* pace_norm_config.norm */
+#define PACE_NORM_NONE 0 /* y = x */
+#define PACE_NORM_L2 1   /* y = x / sqrt(sum_i x_i^2 + eps) */
+#define PACE_NORM_RMS 2  /* y = x / sqrt(sum_i x_i^2 / d + eps) * weight */
+
+/* pace_norm_config.rot_pairs: which channels turn together */
+#define PACE_ROT_HALVES 0   /* i and i + rot / 2 */
+#define PACE_ROT_ADJACENT 1 /* 2 i and 2 i + 1 */
+
+#define PACE_NORM_MAX_D 1024
+
+typedef struct pace_norm_config {
+    int64_t tokens;    /* rows of q, k and pos, >= 0 (0: nothing is done) */
+    int32_t heads_q;   /* query heads, >= 0 (0: q and q_out are not used) */
+    int32_t heads_k;   /* key heads, >= 0 (0: k and k_out are not used) */
+    int32_t d;         /* channels of a head, 1..PACE_NORM_MAX_D */
+    int32_t in_dtype;  /* PACE_DTYPE_*: element type of q, k, q_out, k_out */
+    int32_t norm;      /* PACE_NORM_* */
+    float eps;         /* finite, >= 0 */
+    float q_scale;     /* factor on q_out (e.g. d^-1/2), finite; 1 for none */
+    int32_t rot;       /* leading channels that are rotated: even, 0..d */
+    int32_t rot_pairs; /* PACE_ROT_* */
+    int64_t q_stride;  /* elements between the rows of q, >= heads_q * d */
+    int64_t k_stride;  /* elements between the rows of k, >= heads_k * d */
+} pace_norm_config;
+
+/*
+ * Norms of queries and keys for each head, with the position rotation in the
+ * same pass: what q and k need in front of the decode, prefill and attention
+ * entry points (L2 without rotation for the gated delta rule, which takes
+ * normalised q and k; RMS with rotation is usual for softmax layers).
+ * For each row t and head: x is normalised (see PACE_NORM_*); then, for
+ * i < rot / 2, the pair (a, b) of channels named by rot_pairs becomes
+ *     (a cos w - b sin w, b cos w + a sin w),  w = pos[t] * inv_freq[i];
+ * channels from rot on are not turned; q is multiplied by q_scale.  The angle
+ * is formed and reduced in float64, everything else is float32, rounded once
+ * at the end.
+ *   q: device [tokens] rows of heads_q * d elements, q_stride apart;
+ *   k: likewise (so both can be parts of one packed projection).
+ *   q_weight, k_weight: device float32 [d], or NULL for ones.  PACE_NORM_RMS only.
+ *   pos: device int32 [tokens]; inv_freq: device float32 [rot / 2]; both may
+ *        be NULL if rot = 0.
+ *   q_out: device [tokens, heads_q, d]; k_out: device [tokens, heads_k, d];
+ *        dense.  q_out may be q if q_stride = heads_q * d, k_out likewise;
+ *        otherwise outputs must not overlap inputs.
+ * Any alignment of the element type works; 16-byte aligned rows are fastest.
+ * Errors: EINVAL, EUNSUPPORTED (d), EDEVICE.
+ */
+int pace_qk_norm_rope(const pace_norm_config *cfg, const void *q, const void *k,
+                      const float *q_weight, const float *k_weight, const int32_t *pos,
+                      const float *inv_freq, void *q_out, void *k_out, void *stream);
+
+/*
+ * Linear attention with a fixed decay for each head:
+ *     M_t = decay_h M_{t-1} + k_t v_t^T,   o_t = scale * M_t^T q_t,
+ * over n_tok tokens of every (sequence, head), from a float32 state.  One
+ * entry point for prompts and decode steps: bf16 calls of more than 16 tokens
+ * run a chunked matrix-core kernel (split over the tokens where there are
+ * few states), shorter ones and float32 inputs the recurrent form.
+ *   d_k: 64 or 128; d_v: a multiple of 16, 16..256.
+ *   q, k: device [n_tok, B, H, d_k], v: device [n_tok, B, H, d_v], in_dtype,
+ *         16-byte aligned.
+ *   decay: device float32 [H], 0 <= decay <= 1.
+ *   lens: device int32 [B], or NULL for n_tok each: sequence b has lens[b]
+ *         tokens (clamped to 0..n_tok); tokens behind them are not read and
+ *         their rows of out are left as they were.
+ *   state_in: device float32 [B, H, d_k, d_v], or NULL for zeros.
+ *   state_out: device float32, same shape; receives M after the last token
+ *         (for lens[b] = 0: state_in).  May be state_in.
+ *   out: device float32 [n_tok, B, H, d_v].  state_*, out: 16-byte aligned.
+ *   workspace: device, 16-byte aligned, at least pace_linear_attn_workspace()
+ *         bytes; may be NULL where that is 0.  Its contents do not matter.
+ * All sums and the state are float32.  The chunked kernel splits float32
+ * factors into three bf16 parts (24 significant bits) for the matrix cores.
+ * Errors: EINVAL, EUNSUPPORTED, EDEVICE.
+ */
+int pace_linear_attn(int32_t batch, int32_t heads, int32_t d_k, int32_t d_v, int32_t n_tok,
+                     int32_t in_dtype, const void *q, const void *k, const void *v,
+                     const float *decay, const int32_t *lens, float scale,
+                     const float *state_in, float *state_out, float *out, void *workspace,
+                     uint64_t workspace_bytes, void *stream);
+
+/* Workspace of pace_linear_attn for these sizes, in bytes (0 for decode steps). */
+int pace_linear_attn_workspace(int32_t batch, int32_t heads, int32_t d_k, int32_t d_v,
+                               int32_t n_tok, int32_t in_dtype, uint64_t *out);
+
+/*
+ * A paged KV cache in 4 bits.  Keys and values are held like the recurrent
+ * states: symmetric codes -7..7 with one float32 scale, here for each token,
+ * head and group of PACE_KV4_GROUP channels:
+ *     s = absmax / 7,   c_i = round_to_nearest_even(7 x_i / absmax)
+ * (0 and 0 for a group of zeros).  k and v must be finite.
+ * The caller owns the pool (pace_kv4_pool_bytes bytes of device memory, its
+ * layout is the library's own) and a page table: table[b, i] is the page of
+ * sequence b's tokens i * page_tokens ... (i + 1) * page_tokens - 1, or any
+ * value outside 0..n_pages - 1 for none: tokens there are not written, read
+ * back as zeros and never attended to.  Sequences may share pages to read,
+ * but a page that a call writes must belong to one sequence.
+ */
+#define PACE_KV4_GROUP 64
+
+typedef struct pace_kv4_config {
+    int32_t batch;       /* B: sequences of the call, >= 1 */
+    int32_t heads_q;     /* query heads, a multiple of heads_kv (pace_kv4_attention only) */
+    int32_t heads_kv;    /* key / value heads, >= 1 */
+    int32_t d;           /* channels of a head: 64, 128 or 256 */
+    int32_t page_tokens; /* tokens of a page: a multiple of 32, 32..1024 */
+    int32_t n_pages;     /* pages of the pool, >= 1 */
+    int32_t max_pages;   /* columns of the page table, >= 1 */
+    int32_t in_dtype;    /* PACE_DTYPE_*: element type of q, k, v and the attention's out */
+} pace_kv4_config;
+
+/* Bytes of a pool of cfg.n_pages pages (reads heads_kv, d, page_tokens, n_pages). */
+int pace_kv4_pool_bytes(const pace_kv4_config *cfg, uint64_t *out);
+
+/*
+ * Quantize n_tok tokens of each sequence and write them into the cache:
+ * token t < count[b] of sequence b becomes its cache position start[b] + t.
+ * Positions outside 0..max_pages * page_tokens - 1 are skipped.
+ *   pool: device, 16-byte aligned.  table: device int32 [B, max_pages].
+ *   start: device int32 [B].  count: device int32 [B] (clamped to 0..n_tok)
+ *          or NULL for n_tok each.
+ *   k, v: device [n_tok, B, heads_kv, d], in_dtype, 16-byte aligned.
+ * Errors: EINVAL, EUNSUPPORTED, EDEVICE.
+ */
+int pace_kv4_append(const pace_kv4_config *cfg, void *pool, const int32_t *table,
+                    const int32_t *start, const int32_t *count, int32_t n_tok, const void *k,
+                    const void *v, void *stream);
+
+/*
+ * Read n_tok cached tokens of each sequence back, as the float32 values that
+ * their codes stand for: k_out[t, b] is position start[b] + t.  Tokens
+ * t >= count[b], positions outside the table and tokens without a page give
+ * zeros.
+ *   k_out, v_out: device float32 [n_tok, B, heads_kv, d], 16-byte aligned;
+ *          either may be NULL.  The rest as in pace_kv4_append.
+ * Errors: EINVAL, EUNSUPPORTED, EDEVICE.
+ */
+int pace_kv4_read(const pace_kv4_config *cfg, const void *pool, const int32_t *table,
+                  const int32_t *start, const int32_t *count, int32_t n_tok, float *k_out,
+                  float *v_out, void *stream);
+
+/*
+ * Causal softmax attention over the cache, one token or many per sequence.
+ * Sequence b holds lens[b] tokens, the last count[b] of which are this
+ * call's queries: query t stands at position p = lens[b] - count[b] + t and
+ * sees the positions j <= p (with window > 0 only those with j > p - window
+ * or j < sinks).  Query head h reads key / value head h / (heads_q / heads_kv).
+ *     out = sum_j softmax_j(scale * q . k_j) v_j;
+ * a query that sees nothing gets zeros.
+ *   lens: device int32 [B], clamped to 0..max_pages * page_tokens.
+ *   count: device int32 [B] (clamped to 0..n_tok), or NULL for n_tok each;
+ *          rows t >= count[b] of out are left as they were.
+ *   q, out: device [n_tok, B, heads_q, d], in_dtype, 16-byte aligned.
+ *   scale: finite.  window: >= 0, 0 for none.  sinks: >= 0, used with a window.
+ *   workspace: device, 16-byte aligned, at least
+ *          pace_kv4_attention_workspace() bytes; may be NULL where that is 0.
+ * Scores, softmax statistics and sums are float32.  bf16 calls round the
+ * probabilities to bf16 for the matrix cores (as out is); float32 calls keep
+ * 24 bits of queries and probabilities in three bf16 parts.
+ * Errors: EINVAL, EUNSUPPORTED, EDEVICE.
+ */
+int pace_kv4_attention(const pace_kv4_config *cfg, const void *pool, const int32_t *table,
+                       const int32_t *lens, const int32_t *count, int32_t n_tok, const void *q,
+                       float scale, int32_t window, int32_t sinks, void *out, void *workspace,
+                       uint64_t workspace_bytes, void *stream);
+
+/* Workspace of pace_kv4_attention for these sizes, in bytes. */
+int pace_kv4_attention_workspace(const pace_kv4_config *cfg, int32_t n_tok, uint64_t *out);
+
 /*
  * Measurement utility, not part of the method: copy `bytes` from src to dst
  * (both device, 16-byte aligned, not overlapping; bytes a multiple of 16)

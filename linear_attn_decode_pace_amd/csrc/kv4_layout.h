@@ -1,0 +1,57 @@
+// Layout of the 4-bit paged cache.
+//
+// A page holds, for each key / value head, page_tokens / 32 tiles of 32
+// tokens.  A tile is contiguous: key codes (16 d bytes), value codes (16 d
+// bytes), key scales, value scales (each float32 [d / 64][32], one per group
+// of 64 channels and token).  Codes are stored as c + 8 (1..15), in the order
+// in which the attention kernel's matrix products take them, so that a lane's
+// operand is one 32-bit word of eight codes and a wavefront's load is 1 KiB
+// without gaps:
+//   key codes: word (sub, m) of lane 16 q + t, for token 16 sub + t of the
+//     tile, holds channels 32 m + 8 q + j, j = 0..7 (a k-slice of 32 channels
+//     of the product keys x queries; slices 2 g and 2 g + 1 are group g);
+//   value codes: word c of lane 16 q + n, for channel 16 c + n, holds tokens
+//     4 q + i (i = 0..3) and 16 + 4 q + i (i = 4..7 after subtracting 4) of the
+//     tile: the tokens whose scores that lane holds of the product above.
+// Words are grouped by four: word w of lane l is at ((w / 4) * 64 + l) * 16 +
+// (w % 4) * 4 (w = sub * d / 32 + m for keys).  Inside a word of keys,
+// channel j is nibble (j % 2) * 4 + j / 2; inside a word of values, index i is
+// nibble i: shifting a word right by 4 p then leaves the operand's elements 2 p and
+// 2 p + 1 in bits 3:0 and 19:16.
+#pragma once
+
+#include "pace_layers.h"
+
+namespace pace {
+
+constexpr int KV4_TILE = 32;   // tokens of a tile
+constexpr int KV4_GROUP = 64;  // channels that share a scale
+
+__host__ __device__ inline size_t kv4_tile_bytes(int d) { return (size_t)36 * d; }
+
+__device__ inline int kv4_word_offset(int w, int lane) { return ((w >> 2) * 64 + lane) * 16 + (w & 3) * 4; }
+
+// byte offset in a tile of the word with key (token t, channel c), and its nibble
+__device__ inline int kv4_key_word(int d, int t, int c, int *nibble) {
+    const int j = c & 7;
+    *nibble = (j & 1) * 4 + (j >> 1);
+    return kv4_word_offset((t >> 4) * (d >> 5) + (c >> 5), ((c >> 3) & 3) * 16 + (t & 15));
+}
+// byte offset of the value word, and its nibble
+__device__ inline int kv4_value_word(int d, int t, int c, int *nibble) {
+    *nibble = (t >> 4) * 4 + (t & 3);
+    return 16 * d + kv4_word_offset(c >> 4, ((t & 15) >> 2) * 16 + (c & 15));
+}
+__device__ inline int kv4_key_scales(int d) { return 32 * d; }
+__device__ inline int kv4_value_scales(int d) { return 34 * d; }
+
+// tile `tile` (tokens 32 tile ..) of sequence b, head h; NULL without a page
+__device__ inline uint8_t *kv4_tile(const Kv4View &c, int b, int h, int tile) {
+    const int per = c.page_tokens / KV4_TILE, col = tile / per;
+    if (tile < 0 || col >= c.max_pages) return nullptr;
+    const int page = c.table[(size_t)b * c.max_pages + col];
+    if (page < 0 || page >= c.n_pages) return nullptr;
+    return c.pool + (((size_t)page * c.Hk + h) * per + (tile - col * per)) * kv4_tile_bytes(c.d);
+}
+
+}  // namespace pace

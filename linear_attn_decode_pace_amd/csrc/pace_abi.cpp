@@ -10,14 +10,14 @@
 
 #include <hip/hip_runtime.h>
 
-#include "../../include/pace.h"
 #include "pace_layout.h"
 #include "pace_mfma.h"
 #include "pace_prefill.h"
+#include "pace_status.h"
 #include "pace_step.h"
 #include "pace_window.h"
 
-#define PACE_API extern "C" __attribute__((visibility("default")))
+using namespace pace;
 
 struct pace_state {
     pace_config cfg;
@@ -87,8 +87,10 @@ struct pace_state {
 };
 
 namespace {
-
 thread_local std::string g_err;
+}
+
+namespace pace {
 
 int fail(int code, const char *fmt, ...) {
     char buf[512];
@@ -114,8 +116,6 @@ int hip_fail(hipError_t e, const char *what) {
     return fail(PACE_EDEVICE, "%s: %s", what, hipGetErrorString(e));
 }
 
-bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
 int check_shape(int32_t batch, int32_t heads, int32_t d_k, int32_t d_v) {
     if (batch < 1 || heads < 1) return fail(PACE_EINVAL, "batch and heads must be >= 1");
     if (d_k < 1 || d_v < 1) return fail(PACE_EINVAL, "d_k and d_v must be >= 1");
@@ -131,6 +131,10 @@ int check_dtype(int32_t dt) {
         return fail(PACE_EINVAL, "in_dtype must be PACE_DTYPE_F32 or PACE_DTYPE_BF16");
     return PACE_OK;
 }
+
+}  // namespace pace
+
+namespace {
 
 int check_tokens(int32_t n_tok, int32_t in_dtype, const void *q, const void *k, const void *v,
                  const float *alpha, const float *beta) {

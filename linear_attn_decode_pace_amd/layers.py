@@ -1,0 +1,293 @@
+"""Torch-side calls of the layers beside the gated delta rule.
+
+Head norms with the position rotation, linear attention with a decay for each
+head, and a paged KV cache held in 4 bits with the attention that reads it.
+Every computation runs in libpace.so (include/pace.h documents the formulas);
+this module checks tensors, allocates outputs and workspaces with torch, and
+passes pointers.  ``stream`` is a ``torch.cuda.Stream`` or None for the
+current stream of the tensors' device; outputs and workspaces that a call
+allocates belong to that stream.  Nothing here waits, and calls whose buffers
+are all given can be captured into a graph.
+"""
+from __future__ import annotations
+
+import contextlib
+from typing import Optional, Tuple
+
+import torch
+
+from . import pace
+
+_DTYPES = {torch.bfloat16: pace.PACE_DTYPE_BF16, torch.float32: pace.PACE_DTYPE_F32}
+_NORMS = {"none": pace.PACE_NORM_NONE, "l2": pace.PACE_NORM_L2, "rms": pace.PACE_NORM_RMS}
+_HERE = contextlib.nullcontext()
+
+
+def _dtype(x: torch.Tensor, name: str) -> int:
+    code = _DTYPES.get(x.dtype)
+    if code is None:
+        raise TypeError(f"{name} must be bfloat16 or float32, not {x.dtype}")
+    return code
+
+
+def _check(x, name: str, dtype, shape, device, dense: bool = True) -> None:
+    """x is a device tensor of this type, shape and device, without gaps."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be on a GPU, not on {x.device}")
+    if x.device != device:
+        raise ValueError(f"{name} is on {x.device}, the first tensor on {device}")
+    if x.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, not {x.dtype}")
+    if tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(x.shape)}")
+    if dense and not x.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _first(x, name: str, dims: int) -> torch.device:
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor")
+    if not x.is_cuda:
+        raise ValueError(f"{name} must be on a GPU, not on {x.device}")
+    if x.dim() != dims:
+        raise ValueError(f"{name} must have {dims} dimensions, not {x.dim()}")
+    return x.device
+
+
+def _on(device: torch.device, stream):
+    """Context in which `device` is current, and `stream` its current stream."""
+    if stream is not None:
+        if not isinstance(stream, torch.cuda.Stream):
+            raise TypeError("stream must be a torch.cuda.Stream or None")
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() != device.index:
+        return torch.cuda.device(device)
+    return _HERE
+
+
+def _workspace(given, need: int, device) -> Tuple[Optional[torch.Tensor], int]:
+    if not need:
+        return None, 0
+    if given is None:
+        return torch.empty(need, dtype=torch.uint8, device=device), need
+    if not isinstance(given, torch.Tensor) or given.dtype != torch.uint8 or not given.is_contiguous():
+        raise TypeError("workspace must be a contiguous uint8 tensor")
+    if given.device != device:
+        raise ValueError(f"workspace is on {given.device}, the tensors on {device}")
+    return given, given.numel()
+
+
+# ---- head norms with rotation ----------------------------------------------
+
+def _heads(x, name: str, d: Optional[int]) -> int:
+    """Row stride of x [tokens, heads, d], whose heads are dense."""
+    if x.dim() != 3:
+        raise ValueError(f"{name} must be [tokens, heads, d]")
+    tokens, heads, dd = x.shape
+    if d is not None and dd != d:
+        raise ValueError(f"{name} has {dd} channels, q has {d}")
+    if (dd > 1 and x.stride(2) != 1) or (heads > 1 and x.stride(1) != dd):
+        raise ValueError(f"{name}: the heads of a row must be dense")
+    stride = x.stride(0) if tokens > 1 else heads * dd
+    if stride < heads * dd:
+        raise ValueError(f"{name}: rows overlap")
+    return stride
+
+
+def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None, norm: str = "l2",
+                 q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                 eps: float = 1e-6, q_scale: float = 1.0, pos: Optional[torch.Tensor] = None,
+                 inv_freq: Optional[torch.Tensor] = None, adjacent: bool = False,
+                 q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                 stream=None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Normalise (and rotate) the heads of q [tokens, heads_q, d] and k [tokens,
+    heads_k, d]; rows may be parts of wider ones (a packed projection).  The
+    first 2 * len(inv_freq) channels are rotated by pos[t] * inv_freq[i], in
+    halves, or in adjacent pairs.  Returns dense (q_out, k_out); an output may
+    be its dense input.  See pace_qk_norm_rope."""
+    device = _first(q, "q", 3)
+    code = _dtype(q, "q")
+    tokens, hq, d = q.shape
+    q_stride = _heads(q, "q", None)
+    hk = k_stride = 0
+    if k is not None:
+        k_stride = _heads(k, "k", d)
+        hk = k.shape[1]
+        _check(k, "k", q.dtype, (tokens, hk, d), device, dense=False)
+    if norm not in _NORMS:
+        raise ValueError(f"norm must be one of {sorted(_NORMS)}")
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _check(w, name, torch.float32, (d,), device)
+    rot = 0
+    if inv_freq is not None:
+        _check(inv_freq, "inv_freq", torch.float32, (inv_freq.numel(),), device)
+        rot = 2 * inv_freq.numel()
+        if rot:
+            _check(pos, "pos", torch.int32, (tokens,), device)
+    cfg = pace.pace_norm_config(tokens, hq, hk, d, code, _NORMS[norm], eps, q_scale, rot,
+                                pace.PACE_ROT_ADJACENT if adjacent else pace.PACE_ROT_HALVES,
+                                q_stride, k_stride)
+    with _on(device, stream):
+        if q_out is None:
+            q_out = torch.empty((tokens, hq, d), dtype=q.dtype, device=device)
+        else:
+            _check(q_out, "q_out", q.dtype, (tokens, hq, d), device)
+        if k is None:
+            if k_out is not None:
+                raise ValueError("k_out needs k")
+        elif k_out is None:
+            k_out = torch.empty((tokens, hk, d), dtype=q.dtype, device=device)
+        else:
+            _check(k_out, "k_out", q.dtype, (tokens, hk, d), device)
+        if tokens:
+            pace.pace_qk_norm_rope(cfg, q, k, q_weight, k_weight, pos if rot else None,
+                                   inv_freq if rot else None, q_out, k_out)
+    return q_out, k_out
+
+
+# ---- linear attention with a decay for each head ---------------------------
+
+def linear_attention_workspace(q: torch.Tensor, v: torch.Tensor) -> Optional[torch.Tensor]:
+    """A workspace for linear_attention calls of these shapes (None if none is needed)."""
+    t, b, h, dk = q.shape
+    need = pace.pace_linear_attn_workspace(b, h, dk, v.shape[-1], t, _dtype(q, "q"))
+    return torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+
+
+def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: torch.Tensor,
+                     state: Optional[torch.Tensor] = None, lens: Optional[torch.Tensor] = None,
+                     scale: float = 1.0, out: Optional[torch.Tensor] = None,
+                     state_out: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None,
+                     stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """o_t = scale * M_t^T q_t with M_t = decay_h M_{t-1} + k_t v_t^T over the
+    tokens of q, k [T, B, H, d_k] and v [T, B, H, d_v], from the float32 state
+    [B, H, d_k, d_v] (None: zeros).  lens int32 [B] gives sequences of different
+    lengths; rows of `out` behind them are not written (undefined in an `out`
+    that the call allocates).  Returns (out, state_out), float32; state_out may
+    be state.  See pace_linear_attn."""
+    device = _first(q, "q", 4)
+    code = _dtype(q, "q")
+    t, b, h, dk = q.shape
+    _first(v, "v", 4)
+    dv = v.shape[3]
+    _check(q, "q", q.dtype, (t, b, h, dk), device)
+    _check(k, "k", q.dtype, (t, b, h, dk), device)
+    _check(v, "v", q.dtype, (t, b, h, dv), device)
+    _check(decay, "decay", torch.float32, (h,), device)
+    if state is not None:
+        _check(state, "state", torch.float32, (b, h, dk, dv), device)
+    if lens is not None:
+        _check(lens, "lens", torch.int32, (b,), device)
+    need = pace.pace_linear_attn_workspace(b, h, dk, dv, t, code)
+    with _on(device, stream):
+        if out is None:
+            out = torch.empty((t, b, h, dv), dtype=torch.float32, device=device)
+        else:
+            _check(out, "out", torch.float32, (t, b, h, dv), device)
+        if state_out is None:
+            state_out = torch.empty((b, h, dk, dv), dtype=torch.float32, device=device)
+        else:
+            _check(state_out, "state_out", torch.float32, (b, h, dk, dv), device)
+        ws, n = _workspace(workspace, need, device)
+        pace.pace_linear_attn(b, h, dk, dv, t, code, q, k, v, decay, state_out, out, lens, scale,
+                              state, ws, n)
+    return out, state_out
+
+
+# ---- 4-bit paged KV cache --------------------------------------------------
+
+class Kv4Cache:
+    """The pool of a paged KV cache in 4 bits: `pages` pages of `page_tokens`
+    tokens for `heads_kv` heads of d channels.  Page tables (int32 [B, columns],
+    page numbers, anything outside 0..pages - 1 for none) belong to the caller
+    and are given to each call."""
+
+    def __init__(self, pages: int, heads_kv: int, d: int, page_tokens: int = 64, device="cuda"):
+        self.pages, self.heads_kv, self.d, self.page_tokens = pages, heads_kv, d, page_tokens
+        cfg = pace.pace_kv4_config(0, 0, heads_kv, d, page_tokens, pages, 0, 0)
+        self.pool = torch.empty(pace.pace_kv4_pool_bytes(cfg), dtype=torch.uint8, device=device)
+
+    @property
+    def nbytes(self) -> int:
+        return self.pool.numel()
+
+    def _config(self, table, batch: int, heads_q: int, code: int) -> pace.pace_kv4_config:
+        _first(table, "table", 2)
+        _check(table, "table", torch.int32, (batch, table.shape[1]), self.pool.device)
+        return pace.pace_kv4_config(batch, heads_q, self.heads_kv, self.d, self.page_tokens,
+                                    self.pages, table.shape[1], code)
+
+    def append(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, start: torch.Tensor,
+               count: Optional[torch.Tensor] = None, stream=None) -> None:
+        """Quantize k, v [T, B, heads_kv, d] into positions start[b] + t of the
+        cache, for t < count[b] (None: all T).  See pace_kv4_append."""
+        device = self.pool.device
+        _first(k, "k", 4)
+        t, b = k.shape[0], k.shape[1]
+        cfg = self._config(table, b, 0, _dtype(k, "k"))
+        _check(k, "k", k.dtype, (t, b, self.heads_kv, self.d), device)
+        _check(v, "v", k.dtype, (t, b, self.heads_kv, self.d), device)
+        _check(start, "start", torch.int32, (b,), device)
+        if count is not None:
+            _check(count, "count", torch.int32, (b,), device)
+        with _on(device, stream):
+            pace.pace_kv4_append(cfg, self.pool, table, start, t, k, v, count)
+
+    def read(self, table: torch.Tensor, start: torch.Tensor, n_tok: int,
+             count: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+        """float32 (k, v) [n_tok, B, heads_kv, d]: what the cache holds at
+        positions start[b] + t (zeros for t >= count[b] and without a page)."""
+        device = self.pool.device
+        _first(table, "table", 2)
+        b = table.shape[0]
+        cfg = self._config(table, b, 0, pace.PACE_DTYPE_F32)
+        _check(start, "start", torch.int32, (b,), device)
+        if count is not None:
+            _check(count, "count", torch.int32, (b,), device)
+        if n_tok < 1:
+            raise ValueError("n_tok must be >= 1")
+        with _on(device, stream):
+            k = torch.empty((n_tok, b, self.heads_kv, self.d), dtype=torch.float32, device=device)
+            v = torch.empty_like(k)
+            pace.pace_kv4_read(cfg, self.pool, table, start, n_tok, k, v, count)
+        return k, v
+
+    def attention_workspace(self, q: torch.Tensor, table: torch.Tensor) -> Optional[torch.Tensor]:
+        """A workspace for attention calls with queries and tables of these shapes."""
+        cfg = self._config(table, q.shape[1], q.shape[2], _dtype(q, "q"))
+        need = pace.pace_kv4_attention_workspace(cfg, q.shape[0])
+        return torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+
+    def attention(self, q: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                  count: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                  window: int = 0, sinks: int = 0, out: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Causal softmax attention of q [T, B, heads_q, d] over the lens[b]
+        cached tokens of each sequence, the last count[b] (None: T) of which
+        are the queries' own; window and sinks as in pace_kv4_attention.
+        scale defaults to d ** -0.5.  Returns out, of q's type (rows
+        t >= count[b] are not written)."""
+        device = _first(q, "q", 4)
+        t, b, hq, d = q.shape
+        cfg = self._config(table, b, hq, _dtype(q, "q"))
+        _check(q, "q", q.dtype, (t, b, hq, self.d), self.pool.device)
+        _check(lens, "lens", torch.int32, (b,), device)
+        if count is not None:
+            _check(count, "count", torch.int32, (b,), device)
+        need = pace.pace_kv4_attention_workspace(cfg, t)
+        with _on(device, stream):
+            if out is None:
+                out = torch.empty_like(q)
+            else:
+                _check(out, "out", q.dtype, q.shape, device)
+            ws, n = _workspace(workspace, need, device)
+            pace.pace_kv4_attention(cfg, self.pool, table, lens, t, q,
+                                    d ** -0.5 if scale is None else scale, out, count, window, sinks,
+                                    ws, n)
+        return out

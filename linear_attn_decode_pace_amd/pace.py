@@ -44,10 +44,21 @@ PACE_ADAPTIVE = 0x4
 PACE_FP8_WINDOW = 0x8
 PACE_STATS_MAX_HEADS = 256
 
+PACE_NORM_NONE = 0
+PACE_NORM_L2 = 1
+PACE_NORM_RMS = 2
+PACE_NORM_MAX_D = 1024
+PACE_ROT_HALVES = 0
+PACE_ROT_ADJACENT = 1
+PACE_KV4_GROUP = 64
+
 EXPORTED = ("pace_abi_version", "pace_last_error", "pace_state_alloc", "pace_state_free",
             "pace_state_config", "pace_raw_bytes", "pace_decode_period", "pace_read_state",
             "pace_quant_stats", "pace_prefill_f32", "pace_decode_step", "pace_flush_steps",
-            "pace_prefill_encode", "pace_stream_copy", "pace_quant_stats_static")
+            "pace_prefill_encode", "pace_stream_copy", "pace_quant_stats_static",
+            "pace_qk_norm_rope", "pace_linear_attn", "pace_linear_attn_workspace",
+            "pace_kv4_pool_bytes", "pace_kv4_append", "pace_kv4_read", "pace_kv4_attention",
+            "pace_kv4_attention_workspace")
 
 
 class PaceError(RuntimeError):
@@ -83,6 +94,19 @@ class pace_stats(ctypes.Structure):
         return d
 
 
+class pace_norm_config(ctypes.Structure):
+    _fields_ = [("tokens", ctypes.c_int64), ("heads_q", ctypes.c_int32), ("heads_k", ctypes.c_int32),
+                ("d", ctypes.c_int32), ("in_dtype", ctypes.c_int32), ("norm", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("q_scale", ctypes.c_float), ("rot", ctypes.c_int32),
+                ("rot_pairs", ctypes.c_int32), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64)]
+
+
+class pace_kv4_config(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("batch", "heads_q", "heads_kv", "d", "page_tokens",
+                                              "n_pages", "max_pages", "in_dtype")]
+
+
 def _load():
     # torch first: its bundled HIP runtime carries the same soname as the one
     # libpace.so was linked against, so the loader binds libpace.so to it and
@@ -91,7 +115,8 @@ def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is not built; run `python -m linear_attn_decode_pace_amd.build`")
     lib = ctypes.CDLL(LIB_PATH)
-    vp, i32 = ctypes.c_void_p, ctypes.c_int32
+    vp, i32, f32, u64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_float, ctypes.c_uint64
+    kv4 = ctypes.POINTER(pace_kv4_config)
     sig = {
         "pace_abi_version": ([], ctypes.c_int),
         "pace_last_error": ([], ctypes.c_char_p),
@@ -110,6 +135,15 @@ def _load():
         "pace_prefill_encode": ([vp, i32, vp, vp, vp, vp, vp, vp, vp], ctypes.c_int),
         "pace_stream_copy": ([vp, vp, ctypes.c_uint64, vp], ctypes.c_int),
         "pace_quant_stats_static": ([vp, ctypes.POINTER(pace_stats), vp], ctypes.c_int),
+        "pace_qk_norm_rope": ([ctypes.POINTER(pace_norm_config)] + [vp] * 9, ctypes.c_int),
+        "pace_linear_attn": ([i32] * 6 + [vp] * 5 + [f32] + [vp] * 4 + [u64, vp], ctypes.c_int),
+        "pace_linear_attn_workspace": ([i32] * 6 + [ctypes.POINTER(u64)], ctypes.c_int),
+        "pace_kv4_pool_bytes": ([kv4, ctypes.POINTER(u64)], ctypes.c_int),
+        "pace_kv4_append": ([kv4, vp, vp, vp, vp, i32, vp, vp, vp], ctypes.c_int),
+        "pace_kv4_read": ([kv4, vp, vp, vp, vp, i32, vp, vp, vp], ctypes.c_int),
+        "pace_kv4_attention": ([kv4, vp, vp, vp, vp, i32, vp, f32, i32, i32, vp, vp, u64, vp],
+                               ctypes.c_int),
+        "pace_kv4_attention_workspace": ([kv4, i32, ctypes.POINTER(u64)], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
         fn = getattr(lib, name)
@@ -229,3 +263,57 @@ def pace_prefill_f32(batch: int, heads: int, d_k: int, d_v: int, n_tok: int, in_
     _check(LIB.pace_prefill_f32(batch, heads, d_k, d_v, n_tok, in_dtype, _ptr(q), _ptr(k),
                                 _ptr(v), _ptr(alpha), _ptr(beta), _ptr(state), _ptr(out),
                                 _stream(stream)))
+
+
+def pace_qk_norm_rope(cfg: pace_norm_config, q, k, q_weight, k_weight, pos, inv_freq, q_out, k_out,
+                      stream=None) -> None:
+    _check(LIB.pace_qk_norm_rope(ctypes.byref(cfg), _ptr(q), _ptr(k), _ptr(q_weight), _ptr(k_weight),
+                                 _ptr(pos), _ptr(inv_freq), _ptr(q_out), _ptr(k_out),
+                                 _stream(stream)))
+
+
+def pace_linear_attn_workspace(batch: int, heads: int, d_k: int, d_v: int, n_tok: int,
+                               in_dtype: int) -> int:
+    n = ctypes.c_uint64()
+    _check(LIB.pace_linear_attn_workspace(batch, heads, d_k, d_v, n_tok, in_dtype, ctypes.byref(n)))
+    return n.value
+
+
+def pace_linear_attn(batch: int, heads: int, d_k: int, d_v: int, n_tok: int, in_dtype: int, q, k, v,
+                     decay, state_out, out, lens=None, scale: float = 1.0, state_in=None,
+                     workspace=None, workspace_bytes: int = 0, stream=None) -> None:
+    _check(LIB.pace_linear_attn(batch, heads, d_k, d_v, n_tok, in_dtype, _ptr(q), _ptr(k), _ptr(v),
+                                _ptr(decay), _ptr(lens), scale, _ptr(state_in), _ptr(state_out),
+                                _ptr(out), _ptr(workspace), workspace_bytes, _stream(stream)))
+
+
+def pace_kv4_pool_bytes(cfg: pace_kv4_config) -> int:
+    n = ctypes.c_uint64()
+    _check(LIB.pace_kv4_pool_bytes(ctypes.byref(cfg), ctypes.byref(n)))
+    return n.value
+
+
+def pace_kv4_append(cfg: pace_kv4_config, pool, table, start, n_tok: int, k, v, count=None,
+                    stream=None) -> None:
+    _check(LIB.pace_kv4_append(ctypes.byref(cfg), _ptr(pool), _ptr(table), _ptr(start), _ptr(count),
+                               n_tok, _ptr(k), _ptr(v), _stream(stream)))
+
+
+def pace_kv4_read(cfg: pace_kv4_config, pool, table, start, n_tok: int, k_out, v_out, count=None,
+                  stream=None) -> None:
+    _check(LIB.pace_kv4_read(ctypes.byref(cfg), _ptr(pool), _ptr(table), _ptr(start), _ptr(count),
+                             n_tok, _ptr(k_out), _ptr(v_out), _stream(stream)))
+
+
+def pace_kv4_attention_workspace(cfg: pace_kv4_config, n_tok: int) -> int:
+    n = ctypes.c_uint64()
+    _check(LIB.pace_kv4_attention_workspace(ctypes.byref(cfg), n_tok, ctypes.byref(n)))
+    return n.value
+
+
+def pace_kv4_attention(cfg: pace_kv4_config, pool, table, lens, n_tok: int, q, scale: float, out,
+                       count=None, window: int = 0, sinks: int = 0, workspace=None,
+                       workspace_bytes: int = 0, stream=None) -> None:
+    _check(LIB.pace_kv4_attention(ctypes.byref(cfg), _ptr(pool), _ptr(table), _ptr(lens), _ptr(count),
+                                  n_tok, _ptr(q), scale, window, sinks, _ptr(out), _ptr(workspace),
+                                  workspace_bytes, _stream(stream)))

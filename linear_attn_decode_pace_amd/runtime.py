@@ -11,6 +11,8 @@ import numpy as np
 import torch
 
 from . import inputs, pace
+from .layers import (Kv4Cache, linear_attention, linear_attention_workspace,  # noqa: F401
+                     qk_norm_rope)
 
 
 def dtype_code(w: inputs.Workload) -> int:
