@@ -1,96 +1,495 @@
-// Softmax attention over the 4-bit paged cache.
+// Softmax attention over the 4-bit paged cache, on bf16 matrix cores straight
+// from the codes.
+//
+// For one key / value head, the query rows are the G heads that share it times
+// the call's tokens (row r = token * G + head).  A wavefront takes 16 NT rows and
+// tiles of 32 cached tokens, and works transposed, tokens by rows:
+//   S^T = K Q^T   (16 x 16 x 32 products: A = keys, B = queries),
+//   P   = exp2(S * scale * log2 e - m),
+//   O^T = V^T P   (A = values, B = probabilities).
+// S^T leaves a lane with four tokens of each 16 of one query, which are the
+// operand elements of the second product if its k-slots are taken in that order
+// (kv4_layout.h stores values so): nothing passes through LDS, and the row
+// statistics are a lane's own values plus two lane swaps.
+//
+// Codes.  A nibble n = c + 8 becomes the bf16 16 + n by one shift and one
+// and-or for two codes (exponent 4, n in the upper mantissa bits), so operands
+// hold c + 24.  The constant leaves each product exactly in float32:
+// accumulators of S start at -24 sum(q) of their 64 channels, and O
+// loses 24 sum(p) at the end, with sum(p) of the rounded p from one more
+// product with a tile of ones.  Scales multiply S per token and group, and p
+// per token and group before it is rounded.
+//
+// Row maxima are lazy: a wave rescales its sums only where a score exceeds the
+// row's reference by 2^8 or more, which is exact in float32 and keeps the
+// cross-lane work out of nearly all tiles.
+#include <algorithm>
+
 #include "kv4_layout.h"
 #include "mfma_common.h"
 
 namespace pace {
 namespace {
 
-__device__ inline float code_of(const uint8_t *tile, int off, int nib) {
-    return (float)((int)((*(const uint32_t *)(tile + off) >> (4 * nib)) & 15) - 8);
+constexpr float CODE_BIAS = 24.f;
+
+// eight codes of a word as bf16 c + 24
+__device__ inline bf16x8 biased_codes(uint32_t w) {
+    const uint32_t mask = 0x00780078u, one = 0x41804180u;
+    return __builtin_bit_cast(bf16x8, u32x4{((w << 3) & mask) | one, ((w >> 1) & mask) | one,
+                                            ((w >> 5) & mask) | one, ((w >> 9) & mask) | one});
 }
 
-// One wave per query row: 64 positions at a time, a lane scores one of them;
-// then each lane sums its channels over the 64.
-template <class T>
-__global__ void __launch_bounds__(64) kv4_attention_row_kernel(Kv4AttnArgs a) {
-    __shared__ float q[256], p[64];
-    const Kv4View &c = a.c;
-    const int lane = threadIdx.x, Hq = c.Hk * a.G;
-    const int hq = blockIdx.x % Hq, b = blockIdx.x / Hq % c.B, t = blockIdx.x / Hq / c.B;
-    const int h = hq / a.G, cap = (int)min((long long)c.max_pages * c.page_tokens, 0x7fffffffll);
-    const int len = min(max(a.lens[b], 0), cap), n = a.count ? min(max(a.count[b], 0), a.T) : a.T;
-    if (t >= n) return;
-    const size_t row = (((size_t)t * c.B + b) * Hq + hq) * c.d;
-    for (int i = lane; i < c.d; i += 64)
-        q[i] = sizeof(T) == 2 ? bf2f(((const uint16_t *)a.q)[row + i]) : ((const float *)a.q)[row + i];
-    __syncthreads();
-    const int at = len - n + t;
-    float top = -INFINITY, sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int j0 = 0; j0 <= at; j0 += 64) {
-        const int j = j0 + lane;
-        const bool see = j <= at && (a.window == 0 || j > at - a.window || j < a.sinks);
-        const uint8_t *tile = see ? kv4_tile(c, b, h, j / KV4_TILE) : nullptr;
-        float score = -INFINITY;
-        if (tile) {
-            score = 0.f;
-            const float *sc = (const float *)(tile + kv4_key_scales(c.d));
-            for (int g = 0; g < c.d / KV4_GROUP; ++g) {
-                float dot = 0.f;
-                for (int i = g * KV4_GROUP; i < (g + 1) * KV4_GROUP; ++i) {
-                    int nib;
-                    const int off = kv4_key_word(c.d, j % KV4_TILE, i, &nib);
-                    dot = fmaf(q[i], code_of(tile, off, nib), dot);
-                }
-                score = fmaf(dot, sc[g * KV4_TILE + j % KV4_TILE], score);
-            }
-            score *= a.scale;
-        }
-        float m = score;
+// eight codes of a word as bf16 c, exactly
+__device__ inline bf16x8 exact_codes(uint32_t w) {
+    u32x4 r = __builtin_bit_cast(u32x4, biased_codes(w));
 #pragma unroll
-        for (int x = 1; x < 64; x <<= 1) m = xor_max(m, x);
-        m = fmaxf(m, top);
-        if (m == -INFINITY) continue;
-        const float e = expf(score - m), old = expf(top - m);
-        float es = e;
+    for (int p = 0; p < 4; ++p) {
+        const uint32_t lo = __float_as_uint(lo_f32(r[p]) - CODE_BIAS), hi = __float_as_uint(hi_f32(r[p]) - CODE_BIAS);
+        r[p] = (lo >> 16) | (hi & 0xffff0000u);
+    }
+    return __builtin_bit_cast(bf16x8, r);
+}
+
+// max / sum over the four lanes that share lane % 16
+__device__ inline float quad_max(float x) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
+}
+__device__ inline float quad_sum(float x) {
+    const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    x = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float(b[0]) + __uint_as_float(b[1]);
+}
+
+// a wavefront's share of one tile
+template <int D>
+struct TileRegs {
+    u32x4 k[D / 64], v[D / 64];
+    f32x4 ks[D / 64][2], vs[D / 64][2];   // [group][16-token half]: tokens 4 quad ..
+    __device__ inline void load(const uint8_t *tile, int lane) {
 #pragma unroll
-        for (int x = 1; x < 64; x <<= 1) es += __shfl_xor(es, x);
-        sum = sum * old + es;
-        top = m;
-        __syncthreads();
-        p[lane] = tile ? e : -1.f;
-        __syncthreads();
-        for (int r = 0; r < c.d / 64; ++r) {
-            o[r] *= old;
-            const int ch = r * 64 + lane;
-            for (int x = 0; x < 64; ++x) {
-                if (p[x] < 0.f) continue;
-                const uint8_t *tv = kv4_tile(c, b, h, (j0 + x) / KV4_TILE);
-                int nib;
-                const int off = kv4_value_word(c.d, (j0 + x) % KV4_TILE, ch, &nib);
-                o[r] = fmaf(p[x] * ((const float *)(tv + kv4_value_scales(c.d)))[r * KV4_TILE + (j0 + x) % KV4_TILE],
-                            code_of(tv, off, nib), o[r]);
+        for (int i = 0; i < D / 64; ++i) {
+            k[i] = *(const u32x4 *)(tile + i * 1024 + lane * 16);
+            v[i] = *(const u32x4 *)(tile + 16 * D + i * 1024 + lane * 16);
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                ks[i][s] = *(const f32x4 *)(tile + 32 * D + (i * 32 + s * 16 + (lane >> 4) * 4) * 4);
+                vs[i][s] = *(const f32x4 *)(tile + 34 * D + (i * 32 + s * 16 + (lane >> 4) * 4) * 4);
             }
         }
     }
-    const float inv = sum > 0.f ? 1.f / sum : 0.f;
-    for (int r = 0; r < c.d / 64; ++r) {
-        if constexpr (sizeof(T) == 2)
-            ((uint16_t *)a.out)[row + r * 64 + lane] = (uint16_t)(pk_bf16(o[r] * inv, 0.f) & 0xffff);
-        else
-            ((float *)a.out)[row + r * 64 + lane] = o[r] * inv;
+    __device__ inline uint32_t key_word(int sub, int m) const {
+        const int w = sub * (D / 32) + m;
+        return k[w >> 2][w & 3];
+    }
+    __device__ inline uint32_t value_word(int c) const { return v[c >> 2][c & 3]; }
+};
+
+// What a workgroup works on: 16 NT rows for each of WR row waves, and 4 / WR
+// waves that share a row wave's tiles.
+template <int D, int QP, int NT, int WR>
+struct Attn {
+    static constexpr int NG = D / 64, NM = D / 32, NC = D / 16, WK = 4 / WR;
+    static constexpr bool EXACT = QP == 3;
+    bf16x8 q[NT][QP][NM];
+    float qoff[NT][NG];
+    f32x4 o[NT][NC], psum[NT][NG];
+    float m[NT], l[NT];
+    int at[NT];   // last position that the lane's row sees, -1 for none
+    float c;
+    int window, sinks;
+
+    __device__ inline void step(const TileRegs<D> &t, int p0, bool full, int lane) {
+        bf16x8 ka[2][NM];
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+#pragma unroll
+            for (int i = 0; i < NM; ++i)
+                ka[s][i] = EXACT ? exact_codes(t.key_word(s, i)) : biased_codes(t.key_word(s, i));
+        bf16x8 pb[NT][QP][NG];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            f32x4 sc[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    const float b = EXACT ? 0.f : qoff[nt][g];
+                    f32x4 acc = {b, b, b, b};
+#pragma unroll
+                    for (int i = 2 * g; i < 2 * g + 2; ++i)
+#pragma unroll
+                        for (int part = QP - 1; part >= 0; --part) acc = mfma_bf16_k32(ka[s][i], q[nt][part][i], acc);
+                    if (g == 0) {
+                        sc[s] = acc * t.ks[g][s];
+                    } else {
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) sc[s][r] = fmaf(acc[r], t.ks[g][s][r], sc[s][r]);
+                    }
+                }
+            bool see[2][4];
+            if (!full) {
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const int p = p0 + 16 * s + 4 * (lane >> 4) + r;
+                        see[s][r] = p <= at[nt] && (window == 0 || p > at[nt] - window || p < sinks);
+                        sc[s][r] = see[s][r] ? sc[s][r] : -INFINITY;
+                    }
+            }
+            float top = sc[0][0];
+#pragma unroll
+            for (int e = 1; e < 8; ++e) top = fmaxf(top, sc[e >> 2][e & 3]);
+            if (__any(top * c > m[nt] + 8.f)) {
+                const float m2 = fmaxf(m[nt], quad_max(top) * c);
+                const float f = m2 > m[nt] ? __builtin_amdgcn_exp2f(m[nt] - m2) : 1.f;
+                m[nt] = m2;
+                l[nt] *= f;
+#pragma unroll
+                for (int i = 0; i < NC; ++i) o[nt][i] *= f;
+#pragma unroll
+                for (int g = 0; g < NG; ++g) psum[nt][g] *= f;
+            }
+            const float mm = m[nt] == -INFINITY ? 0.f : m[nt];
+            float p[2][4];
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    p[s][r] = __builtin_amdgcn_exp2f(fmaf(sc[s][r], c, -mm));
+                    l[nt] += p[s][r];
+                }
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                float x[2][4];
+#pragma unroll
+                for (int s = 0; s < 2; ++s)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        x[s][r] = p[s][r] * t.vs[g][s][r];
+                        if (!full) x[s][r] = see[s][r] ? x[s][r] : 0.f;   // scales of unseen tokens may be anything
+                    }
+#pragma unroll
+                for (int part = 0; part < QP; ++part) {
+                    u32x4 w;
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        w[r] = pk_bf16(x[0][r], x[1][r]);
+                        if (part + 1 < QP) {
+                            x[0][r] -= lo_f32(w[r]);
+                            x[1][r] -= hi_f32(w[r]);
+                        }
+                    }
+                    pb[nt][part][g] = __builtin_bit_cast(bf16x8, w);
+                }
+            }
+        }
+        if constexpr (!EXACT) {
+            const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int g = 0; g < NG; ++g) psum[nt][g] = mfma_bf16_k32(ones, pb[nt][0][g], psum[nt][g]);
+        }
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            const bf16x8 va = EXACT ? exact_codes(t.value_word(i)) : biased_codes(t.value_word(i));
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int part = QP - 1; part >= 0; --part)
+                    o[nt][i] = mfma_bf16_k32(va, pb[nt][part][i >> 2], o[nt][i]);
+        }
+    }
+};
+
+// partial results of a split: [splits][B * Hk][R][D + 4] floats: sums, then (m, l)
+__device__ inline float *partial_row(const Kv4AttnArgs &a, int D, int split, int bh, int r) {
+    const size_t R = (size_t)a.T * a.G;
+    return a.workspace + (((size_t)split * a.c.B * a.c.Hk + bh) * R + r) * (D + 4);
+}
+
+template <int QP>
+__device__ inline void store4(void *out, size_t i, f32x4 x) {
+    if constexpr (QP == 1)
+        *(u32x2 *)((uint16_t *)out + i) = u32x2{pk_bf16(x[0], x[1]), pk_bf16(x[2], x[3])};
+    else
+        *(f32x4 *)((float *)out + i) = x;
+}
+
+template <int D, int QP, int NT, int WR>
+__global__ void __launch_bounds__(256) kv4_attention_kernel(Kv4AttnArgs a, int row_blocks, int splits) {
+    using A = Attn<D, QP, NT, WR>;
+    constexpr int ROWS = 16 * NT * WR, LDW = D + 4;
+    const Kv4View &c = a.c;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n16 = lane & 15, quad = lane >> 4;
+    const int wr = wave / A::WK, wk = wave % A::WK;
+    const int BH = c.B * c.Hk, R = a.T * a.G;
+    // (sequence, head) runs fastest: the row blocks that share a head's cache
+    // then meet in one XCD's L2 where B * Hk is a multiple of 8; the last rows,
+    // which see most, come first
+    const int bh = blockIdx.x % BH, rest = blockIdx.x / BH;
+    const int split = rest % splits, rb = row_blocks - 1 - rest / splits;
+    const int b = bh / c.Hk, h = bh - b * c.Hk;
+    const int cap = c.max_pages * c.page_tokens;
+    const int len = min(max(a.lens[b], 0), cap), n = a.count ? min(max(a.count[b], 0), a.T) : a.T;
+    if (rb * ROWS / a.G >= n) return;   // all rows behind the sequence's queries
+    const int r0 = rb * ROWS + wr * 16 * NT;
+
+    A w;
+    w.window = a.window, w.sinks = a.sinks;
+    const float sign = a.scale < 0.f ? -1.f : 1.f;
+    w.c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int r = r0 + nt * 16 + n16, t = r / a.G;
+        const bool ok = r < R && t < n;
+        w.at[nt] = ok ? len - n + t : -1;
+        const size_t row = (((size_t)t * c.B + b) * c.Hk * a.G + (size_t)h * a.G + (r - t * a.G)) * D;
+#pragma unroll
+        for (int g = 0; g < A::NG; ++g) {
+            float sum = 0.f;
+#pragma unroll
+            for (int i = 2 * g; i < 2 * g + 2; ++i) {
+                const size_t at = row + 32 * i + 8 * quad;
+                float x[8];
+                if constexpr (QP == 1) {
+                    u32x4 v = {0, 0, 0, 0};
+                    if (ok) v = *(const u32x4 *)((const uint16_t *)a.q + at);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[2 * e] = lo_f32(v[e]) * sign, x[2 * e + 1] = hi_f32(v[e]) * sign;
+                } else {
+                    f32x4 v0 = {0.f, 0.f, 0.f, 0.f}, v1 = v0;
+                    if (ok) v0 = *(const f32x4 *)((const float *)a.q + at), v1 = *(const f32x4 *)((const float *)a.q + at + 4);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[e] = v0[e] * sign, x[e + 4] = v1[e] * sign;
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) sum += x[e];
+#pragma unroll
+                for (int part = 0; part < QP; ++part) {
+                    u32x4 v;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        v[e] = pk_bf16(x[2 * e], x[2 * e + 1]);
+                        x[2 * e] -= lo_f32(v[e]);
+                        x[2 * e + 1] -= hi_f32(v[e]);
+                    }
+                    w.q[nt][part][i] = __builtin_bit_cast(bf16x8, v);
+                }
+            }
+            w.qoff[nt][g] = -CODE_BIAS * quad_sum(sum);
+            w.psum[nt][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+#pragma unroll
+        for (int i = 0; i < A::NC; ++i) w.o[nt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        w.m[nt] = -INFINITY, w.l[nt] = 0.f;
+    }
+
+    // tiles that some row of the wave sees: those of the sinks, then from the
+    // first row's window to the last row's position
+    const int t_lo = r0 / a.G, t_hi = min((r0 + 16 * NT - 1) / a.G, n - 1);
+    const int at_lo = len - n + t_lo, at_hi = t_lo <= t_hi ? len - n + t_hi : -1;
+    const int end = at_hi < 0 ? 0 : at_hi / KV4_TILE + 1;
+    const int n_sink = a.window ? min((a.sinks + KV4_TILE - 1) / KV4_TILE, end) : 0;
+    const int lo = a.window ? min(max(max(at_lo - a.window + 1, 0) / KV4_TILE, n_sink), end) : 0;
+    const int total = n_sink + end - lo;
+    const int per = (total + splits - 1) / splits;
+    const int first = min(split * per, total), last = min(first + per, total);
+
+    auto tile_of = [&](int i) { return i < n_sink ? i : lo + i - n_sink; };
+    TileRegs<D> buf[2];
+    const uint8_t *next = nullptr;
+    int i = first + wk;
+    if (i < last) next = kv4_tile(c, b, h, tile_of(i));
+    if (next) buf[0].load(next, lane);
+    auto turn = [&](TileRegs<D> &cur, TileRegs<D> &nxt) {
+        const uint8_t *now = next;
+        const int tile = tile_of(i), p0 = tile * KV4_TILE;
+        i += A::WK;
+        next = i < last ? kv4_tile(c, b, h, tile_of(i)) : nullptr;
+        if (next) nxt.load(next, lane);
+        if (now) {
+            const bool full = p0 + KV4_TILE - 1 <= at_lo &&
+                              (a.window == 0 || p0 > at_hi - a.window || p0 + KV4_TILE <= a.sinks);
+            if (full)
+                w.step(cur, p0, true, lane);
+            else
+                w.step(cur, p0, false, lane);
+        }
+    };
+    while (i < last) {
+        turn(buf[0], buf[1]);
+        if (i >= last) break;
+        turn(buf[1], buf[0]);
+    }
+
+    // the four lanes of a row hold its sums in parts
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        w.l[nt] = quad_sum(w.l[nt]);
+        if constexpr (!A::EXACT) {
+#pragma unroll
+            for (int x = 0; x < A::NC; ++x) w.o[nt][x] -= CODE_BIAS * w.psum[nt][x >> 2];
+        }
+    }
+    const size_t out_row = ((size_t)b * c.Hk + h) * a.G;   // + t * B * Hk * G + head
+    if constexpr (A::WK == 1) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = r0 + nt * 16 + n16, t = r / a.G;
+            if (r >= R || t >= n) continue;
+            if (splits == 1) {
+                const float inv = w.l[nt] > 0.f ? 1.f / w.l[nt] : 0.f;
+                const size_t at = ((size_t)t * BH * a.G + out_row + (r - t * a.G)) * D;
+#pragma unroll
+                for (int x = 0; x < A::NC; ++x) store4<QP>(a.out, at + 16 * x + 4 * quad, w.o[nt][x] * inv);
+            } else {
+                float *p = partial_row(a, D, split, bh, r);
+#pragma unroll
+                for (int x = 0; x < A::NC; ++x) *(f32x4 *)(p + 16 * x + 4 * quad) = w.o[nt][x];
+                if (quad == 0) *(f32x2 *)(p + D) = f32x2{w.m[nt], w.l[nt]};
+            }
+        }
+    } else {
+        __shared__ float part[4][16][LDW];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            if (nt) __syncthreads();
+            float *mine = part[wave][n16];
+#pragma unroll
+            for (int x = 0; x < A::NC; ++x) *(f32x4 *)(mine + 16 * x + 4 * quad) = w.o[nt][x];
+            if (quad == 0) mine[D] = w.m[nt], mine[D + 1] = w.l[nt];
+            __syncthreads();
+            for (int u = threadIdx.x; u < WR * 16 * (D / 4); u += 256) {
+                const int x = u % (D / 4), row = u / (D / 4), g = row / 16, rr = row % 16;
+                const int r = rb * ROWS + g * 16 * NT + nt * 16 + rr, t = r / a.G;
+                if (r >= R || t >= n) continue;
+                float top = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < A::WK; ++k) top = fmaxf(top, part[g * A::WK + k][rr][D]);
+                f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+                float l = 0.f;
+#pragma unroll
+                for (int k = 0; k < A::WK; ++k) {
+                    const float *p = part[g * A::WK + k][rr];
+                    const float f = p[D] > -INFINITY ? __builtin_amdgcn_exp2f(p[D] - top) : 0.f;
+                    sum += f * *(const f32x4 *)(p + 4 * x);
+                    l = fmaf(f, p[D + 1], l);
+                }
+                if (splits == 1) {
+                    const float inv = l > 0.f ? 1.f / l : 0.f;
+                    store4<QP>(a.out, ((size_t)t * BH * a.G + out_row + (r - t * a.G)) * D + 4 * x, sum * inv);
+                } else {
+                    float *p = partial_row(a, D, split, bh, r);
+                    *(f32x4 *)(p + 4 * x) = sum;
+                    if (x == 0) *(f32x2 *)(p + D) = f32x2{top, l};
+                }
+            }
+        }
+    }
+}
+
+// Joins the splits of one row: wave w takes splits w, w + 4, ...
+template <int D, int QP>
+__global__ void __launch_bounds__(256) kv4_join_kernel(Kv4AttnArgs a, int splits) {
+    constexpr int NL = D / 4;   // lanes that hold a row
+    __shared__ float part[4][D + 4];
+    const int R = a.T * a.G, bh = blockIdx.x / R, r = blockIdx.x - bh * R, t = r / a.G, b = bh / a.c.Hk;
+    const int n = a.count ? min(max(a.count[b], 0), a.T) : a.T;
+    if (t >= n) return;
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
+    f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+    float top = -INFINITY, l = 0.f;
+    for (int s = wave; s < splits; s += 4) {
+        const float *p = partial_row(a, D, s, bh, r);
+        const f32x2 ml = *(const f32x2 *)(p + D);
+        const f32x4 x = lane < NL ? *(const f32x4 *)(p + 4 * lane) : sum;
+        if (ml[0] == -INFINITY) continue;
+        const float m2 = fmaxf(top, ml[0]);
+        const float f0 = __builtin_amdgcn_exp2f(top - m2), f1 = __builtin_amdgcn_exp2f(ml[0] - m2);
+        sum = sum * f0 + x * f1;
+        l = l * f0 + ml[1] * f1;
+        top = m2;
+    }
+    if (lane < NL) *(f32x4 *)&part[wave][4 * lane] = sum;
+    if (lane == 0) part[wave][D] = top, part[wave][D + 1] = l;
+    __syncthreads();
+    if (threadIdx.x >= NL) return;
+    top = fmaxf(fmaxf(part[0][D], part[1][D]), fmaxf(part[2][D], part[3][D]));
+    sum = f32x4{0.f, 0.f, 0.f, 0.f}, l = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const float f = part[k][D] > -INFINITY ? __builtin_amdgcn_exp2f(part[k][D] - top) : 0.f;
+        sum += f * *(const f32x4 *)&part[k][4 * threadIdx.x];
+        l = fmaf(f, part[k][D + 1], l);
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    store4<QP>(a.out, (((size_t)t * a.c.B * a.c.Hk + bh) * a.G + (r - t * a.G)) * D + 4 * threadIdx.x, sum * inv);
+}
+
+// rows of a workgroup, and the number of parts a row's tokens are split into
+struct Plan {
+    int nt, wr, row_blocks, splits;
+};
+Plan plan_for(const Kv4View &c, int G, int T, int window, int bf16) {
+    Plan p;
+    const long long R = (long long)T * G;
+    const bool wide = bf16 && c.d <= 128;   // registers for two row tiles a wave
+    p.nt = wide && R > 32 ? 2 : 1;
+    p.wr = R <= 16 ? 1 : (R <= 32 || (wide && R <= 64)) ? 2 : 4;
+    p.row_blocks = (int)((R + 16 * p.nt * p.wr - 1) / (16 * p.nt * p.wr));
+    const long long tiles = ((long long)c.max_pages * c.page_tokens + KV4_TILE - 1) / KV4_TILE;
+    const long long groups = (long long)c.B * c.Hk * p.row_blocks;
+    // enough workgroups to fill the card a few times over, but at least four
+    // tiles for each wave
+    const long long want = (4096 + groups - 1) / groups, most = tiles / (4 * (4 / p.wr));
+    p.splits = (int)std::max(1ll, std::min(std::min(want, most), 256ll));
+    (void)window;
+    return p;
+}
+
+template <int D, int QP, int NT, int WR>
+void launch(const Kv4AttnArgs &a, const Plan &p, hipStream_t s) {
+    const dim3 grid((unsigned)((long long)a.c.B * a.c.Hk * p.row_blocks * p.splits));
+    hipLaunchKernelGGL((kv4_attention_kernel<D, QP, NT, WR>), grid, dim3(256), 0, s, a, p.row_blocks, p.splits);
+    if (p.splits > 1)
+        hipLaunchKernelGGL((kv4_join_kernel<D, QP>), dim3((unsigned)((long long)a.c.B * a.c.Hk * a.T * a.G)), dim3(256),
+                           0, s, a, p.splits);
+}
+
+template <int D, int QP>
+void dispatch(const Kv4AttnArgs &a, const Plan &p, hipStream_t s) {
+    if constexpr (QP == 1 && D <= 128) {
+        if (p.nt == 2) return p.wr == 2 ? launch<D, QP, 2, 2>(a, p, s) : launch<D, QP, 2, 4>(a, p, s);
+        return p.wr == 1 ? launch<D, QP, 1, 1>(a, p, s) : launch<D, QP, 1, 2>(a, p, s);
+    } else {
+        if (p.wr == 1) return launch<D, QP, 1, 1>(a, p, s);
+        return p.wr == 2 ? launch<D, QP, 1, 2>(a, p, s) : launch<D, QP, 1, 4>(a, p, s);
     }
 }
 
 }  // namespace
 
-uint64_t kv4_attention_workspace(const Kv4View &, int, int, int) { return 0; }
+uint64_t kv4_attention_workspace(const Kv4View &c, int G, int T, int bf16) {
+    const Plan p = plan_for(c, G, T, 0, bf16);
+    return p.splits == 1 ? 0 : (uint64_t)p.splits * c.B * c.Hk * T * G * (c.d + 4) * 4;
+}
 
 hipError_t launch_kv4_attention(const Kv4AttnArgs &a, int bf16, hipStream_t s) {
-    const dim3 grid((unsigned)((long long)a.T * a.c.B * a.c.Hk * a.G));
-    if (bf16)
-        hipLaunchKernelGGL(kv4_attention_row_kernel<uint16_t>, grid, dim3(64), 0, s, a);
+    const Plan p = plan_for(a.c, a.G, a.T, a.window, bf16);
+    if (a.c.d == 64)
+        bf16 ? dispatch<64, 1>(a, p, s) : dispatch<64, 3>(a, p, s);
+    else if (a.c.d == 128)
+        bf16 ? dispatch<128, 1>(a, p, s) : dispatch<128, 3>(a, p, s);
     else
-        hipLaunchKernelGGL(kv4_attention_row_kernel<float>, grid, dim3(64), 0, s, a);
+        bf16 ? dispatch<256, 1>(a, p, s) : dispatch<256, 3>(a, p, s);
     return hipGetLastError();
 }
 
