@@ -33,16 +33,22 @@ namespace {
 
 constexpr float CODE_BIAS = 24.f;
 
+// The and-or's constants, one in a scalar and one in a vector register: the
+// instruction takes one scalar operand and no literal.
+struct CodeBits {
+    uint32_t mask = 0x00780078u, one = 0x41804180u;
+    __device__ inline CodeBits() { asm volatile("" : "+s"(mask), "+v"(one)); }
+};
+
 // eight codes of a word as bf16 c + 24
-__device__ inline bf16x8 biased_codes(uint32_t w) {
-    const uint32_t mask = 0x00780078u, one = 0x41804180u;
-    return __builtin_bit_cast(bf16x8, u32x4{((w << 3) & mask) | one, ((w >> 1) & mask) | one,
-                                            ((w >> 5) & mask) | one, ((w >> 9) & mask) | one});
+__device__ inline bf16x8 biased_codes(uint32_t w, const CodeBits &k) {
+    return __builtin_bit_cast(bf16x8, u32x4{((w << 3) & k.mask) | k.one, ((w >> 1) & k.mask) | k.one,
+                                            ((w >> 5) & k.mask) | k.one, ((w >> 9) & k.mask) | k.one});
 }
 
 // eight codes of a word as bf16 c, exactly
-__device__ inline bf16x8 exact_codes(uint32_t w) {
-    u32x4 r = __builtin_bit_cast(u32x4, biased_codes(w));
+__device__ inline bf16x8 exact_codes(uint32_t w, const CodeBits &k) {
+    u32x4 r = __builtin_bit_cast(u32x4, biased_codes(w, k));
 #pragma unroll
     for (int p = 0; p < 4; ++p) {
         const uint32_t lo = __float_as_uint(lo_f32(r[p]) - CODE_BIAS), hi = __float_as_uint(hi_f32(r[p]) - CODE_BIAS);
@@ -65,22 +71,20 @@ __device__ inline float quad_sum(float x) {
     return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-// a wavefront's share of one tile
+// a wavefront's share of one tile: its operand words, and D / 64 of the tile's
+// 2 D scales, which the wave spreads through LDS when it comes to the tile
 template <int D>
 struct TileRegs {
+    typedef float scales_t __attribute__((ext_vector_type(D / 64)));
     u32x4 k[D / 64], v[D / 64];
-    f32x4 ks[D / 64][2], vs[D / 64][2];   // [group][16-token half]: tokens 4 quad ..
+    scales_t sc;
     __device__ inline void load(const uint8_t *tile, int lane) {
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
             k[i] = *(const u32x4 *)(tile + i * 1024 + lane * 16);
             v[i] = *(const u32x4 *)(tile + 16 * D + i * 1024 + lane * 16);
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                ks[i][s] = *(const f32x4 *)(tile + 32 * D + (i * 32 + s * 16 + (lane >> 4) * 4) * 4);
-                vs[i][s] = *(const f32x4 *)(tile + 34 * D + (i * 32 + s * 16 + (lane >> 4) * 4) * 4);
-            }
         }
+        sc = *(const scales_t *)(tile + 32 * D + lane * (D / 16));
     }
     __device__ inline uint32_t key_word(int sub, int m) const {
         const int w = sub * (D / 32) + m;
@@ -96,41 +100,53 @@ struct Attn {
     static constexpr int NG = D / 64, NM = D / 32, NC = D / 16, WK = 4 / WR;
     static constexpr bool EXACT = QP == 3;
     bf16x8 q[NT][QP][NM];
-    float qoff[NT][NG];
+    f32x4 qoff[NT][NG];
     f32x4 o[NT][NC], psum[NT][NG];
     float m[NT], l[NT];
     int at[NT];   // last position that the lane's row sees, -1 for none
     float c;
     int window, sinks;
+    CodeBits bits;
+    float *lds;   // the wave's D floats: key scales [group][token], then value scales
 
     __device__ inline void step(const TileRegs<D> &t, int p0, bool full, int lane) {
-        bf16x8 ka[2][NM];
+        *(typename TileRegs<D>::scales_t *)(lds + lane * NG) = t.sc;
+        wave_sync();
+        f32x4 sc[NT][2];
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
+        for (int s = 0; s < 2; ++s) {
+            bf16x8 ka[NM];
 #pragma unroll
             for (int i = 0; i < NM; ++i)
-                ka[s][i] = EXACT ? exact_codes(t.key_word(s, i)) : biased_codes(t.key_word(s, i));
-        bf16x8 pb[NT][QP][NG];
+                ka[i] = EXACT ? exact_codes(t.key_word(s, i), bits) : biased_codes(t.key_word(s, i), bits);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            f32x4 sc[2];
+            for (int g = 0; g < NG; ++g) {
+                const f32x4 ks = *(const f32x4 *)(lds + g * 32 + s * 16 + (lane >> 4) * 4);   // tokens 4 quad ..
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-#pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    const float b = EXACT ? 0.f : qoff[nt][g];
-                    f32x4 acc = {b, b, b, b};
+                for (int nt = 0; nt < NT; ++nt) {
+                    f32x4 acc = EXACT ? f32x4{0.f, 0.f, 0.f, 0.f} : qoff[nt][g];
 #pragma unroll
                     for (int i = 2 * g; i < 2 * g + 2; ++i)
 #pragma unroll
-                        for (int part = QP - 1; part >= 0; --part) acc = mfma_bf16_k32(ka[s][i], q[nt][part][i], acc);
+                        for (int part = QP - 1; part >= 0; --part) acc = mfma_bf16_k32(ka[i], q[nt][part][i], acc);
                     if (g == 0) {
-                        sc[s] = acc * t.ks[g][s];
+                        sc[nt][s] = acc * ks;
                     } else {
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) sc[s][r] = fmaf(acc[r], t.ks[g][s][r], sc[s][r]);
+                        for (int r = 0; r < 4; ++r) sc[nt][s][r] = fmaf(acc[r], ks[r], sc[nt][s][r]);
                     }
                 }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        f32x4 vs[NG][2];
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int s = 0; s < 2; ++s) vs[g][s] = *(const f32x4 *)(lds + D / 2 + g * 32 + s * 16 + (lane >> 4) * 4);
+        bf16x8 pb[NT][QP][NG];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
             bool see[2][4];
             if (!full) {
 #pragma unroll
@@ -139,12 +155,12 @@ struct Attn {
                     for (int r = 0; r < 4; ++r) {
                         const int p = p0 + 16 * s + 4 * (lane >> 4) + r;
                         see[s][r] = p <= at[nt] && (window == 0 || p > at[nt] - window || p < sinks);
-                        sc[s][r] = see[s][r] ? sc[s][r] : -INFINITY;
+                        sc[nt][s][r] = see[s][r] ? sc[nt][s][r] : -INFINITY;
                     }
             }
-            float top = sc[0][0];
+            float top = sc[nt][0][0];
 #pragma unroll
-            for (int e = 1; e < 8; ++e) top = fmaxf(top, sc[e >> 2][e & 3]);
+            for (int e = 1; e < 8; ++e) top = fmaxf(top, sc[nt][e >> 2][e & 3]);
             if (__any(top * c > m[nt] + 8.f)) {
                 const float m2 = fmaxf(m[nt], quad_max(top) * c);
                 const float f = m2 > m[nt] ? __builtin_amdgcn_exp2f(m[nt] - m2) : 1.f;
@@ -161,7 +177,7 @@ struct Attn {
             for (int s = 0; s < 2; ++s)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    p[s][r] = __builtin_amdgcn_exp2f(fmaf(sc[s][r], c, -mm));
+                    p[s][r] = __builtin_amdgcn_exp2f(fmaf(sc[nt][s][r], c, -mm));
                     l[nt] += p[s][r];
                 }
 #pragma unroll
@@ -171,7 +187,7 @@ struct Attn {
                 for (int s = 0; s < 2; ++s)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        x[s][r] = p[s][r] * t.vs[g][s][r];
+                        x[s][r] = p[s][r] * vs[g][s][r];
                         if (!full) x[s][r] = see[s][r] ? x[s][r] : 0.f;   // scales of unseen tokens may be anything
                     }
 #pragma unroll
@@ -189,6 +205,7 @@ struct Attn {
                 }
             }
         }
+        __builtin_amdgcn_sched_barrier(0);
         if constexpr (!EXACT) {
             const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
 #pragma unroll
@@ -198,7 +215,7 @@ struct Attn {
         }
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            const bf16x8 va = EXACT ? exact_codes(t.value_word(i)) : biased_codes(t.value_word(i));
+            const bf16x8 va = EXACT ? exact_codes(t.value_word(i), bits) : biased_codes(t.value_word(i), bits);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -222,10 +239,11 @@ __device__ inline void store4(void *out, size_t i, f32x4 x) {
         *(f32x4 *)((float *)out + i) = x;
 }
 
-template <int D, int QP, int NT, int WR>
-__global__ void __launch_bounds__(256) kv4_attention_kernel(Kv4AttnArgs a, int row_blocks, int splits) {
+template <int D, int QP, int NT, int WR, int PF, int WAVES>
+__global__ void __launch_bounds__(256, WAVES) kv4_attention_kernel(Kv4AttnArgs a, int row_blocks, int splits) {
     using A = Attn<D, QP, NT, WR>;
     constexpr int ROWS = 16 * NT * WR, LDW = D + 4;
+    __shared__ float scales[4][D];
     const Kv4View &c = a.c;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n16 = lane & 15, quad = lane >> 4;
@@ -243,7 +261,7 @@ __global__ void __launch_bounds__(256) kv4_attention_kernel(Kv4AttnArgs a, int r
     const int r0 = rb * ROWS + wr * 16 * NT;
 
     A w;
-    w.window = a.window, w.sinks = a.sinks;
+    w.window = a.window, w.sinks = a.sinks, w.lds = scales[wave];
     const float sign = a.scale < 0.f ? -1.f : 1.f;
     w.c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
 #pragma unroll
@@ -284,7 +302,8 @@ __global__ void __launch_bounds__(256) kv4_attention_kernel(Kv4AttnArgs a, int r
                     w.q[nt][part][i] = __builtin_bit_cast(bf16x8, v);
                 }
             }
-            w.qoff[nt][g] = -CODE_BIAS * quad_sum(sum);
+            const float off = -CODE_BIAS * quad_sum(sum);
+            w.qoff[nt][g] = f32x4{off, off, off, off};
             w.psum[nt][g] = f32x4{0.f, 0.f, 0.f, 0.f};
         }
 #pragma unroll
@@ -304,30 +323,44 @@ __global__ void __launch_bounds__(256) kv4_attention_kernel(Kv4AttnArgs a, int r
     const int first = min(split * per, total), last = min(first + per, total);
 
     auto tile_of = [&](int i) { return i < n_sink ? i : lo + i - n_sink; };
-    TileRegs<D> buf[2];
-    const uint8_t *next = nullptr;
-    int i = first + wk;
-    if (i < last) next = kv4_tile(c, b, h, tile_of(i));
-    if (next) buf[0].load(next, lane);
-    auto turn = [&](TileRegs<D> &cur, TileRegs<D> &nxt) {
-        const uint8_t *now = next;
-        const int tile = tile_of(i), p0 = tile * KV4_TILE;
-        i += A::WK;
-        next = i < last ? kv4_tile(c, b, h, tile_of(i)) : nullptr;
-        if (next) nxt.load(next, lane);
-        if (now) {
+    const int per_page = c.page_tokens / KV4_TILE;
+    // table entries come by scalar loads, which do not stand in the tiles' queue
+    typedef const __attribute__((address_space(4))) int32_t *scalar_ptr;
+    const scalar_ptr table = (scalar_ptr)(uintptr_t)(c.table + (size_t)b * c.max_pages);
+    auto page_of = [&](int tile) { return table[kv4_column(c, tile)]; };
+    // PF tiles in flight: while the wave works on one, the loads of the next
+    // PF - 1 are under way and the table entry of the one behind them is read
+    // (past the last tile, and where a tile has no page, the pool's first tile
+    // is loaded and not used: loads without branches can be waited for one by one)
+    TileRegs<D> buf[PF];
+    bool live[PF];
+    int i = first + wk, ahead = i;
+    int page = ahead < last ? page_of(tile_of(ahead)) : -1;
+    auto fetch = [&](int j) {   // tile `ahead` into slot j
+        const int tile = tile_of(ahead);
+        live[j] = page >= 0 && page < c.n_pages;
+        const size_t at = ((size_t)(uint32_t)page * c.Hk + h) * per_page + (tile - kv4_column(c, tile) * per_page);
+        buf[j].load(c.pool + (live[j] ? at * kv4_tile_bytes(D) : 0), lane);
+        ahead += A::WK;
+        page = ahead < last ? page_of(tile_of(ahead)) : -1;
+    };
+#pragma unroll
+    for (int j = 0; j < PF - 1; ++j) fetch(j);
+    while (i < last) {
+#pragma unroll
+        for (int j = 0; j < PF; ++j) {
+            if (i >= last) break;
+            fetch((j + PF - 1) % PF);
+            const int p0 = tile_of(i) * KV4_TILE;
+            i += A::WK;
+            if (!live[j]) continue;
             const bool full = p0 + KV4_TILE - 1 <= at_lo &&
                               (a.window == 0 || p0 > at_hi - a.window || p0 + KV4_TILE <= a.sinks);
             if (full)
-                w.step(cur, p0, true, lane);
+                w.step(buf[j], p0, true, lane);
             else
-                w.step(cur, p0, false, lane);
+                w.step(buf[j], p0, false, lane);
         }
-    };
-    while (i < last) {
-        turn(buf[0], buf[1]);
-        if (i >= last) break;
-        turn(buf[1], buf[0]);
     }
 
     // the four lanes of a row hold its sums in parts
@@ -458,7 +491,8 @@ Plan plan_for(const Kv4View &c, int G, int T, int window, int bf16) {
 template <int D, int QP, int NT, int WR>
 void launch(const Kv4AttnArgs &a, const Plan &p, hipStream_t s) {
     const dim3 grid((unsigned)((long long)a.c.B * a.c.Hk * p.row_blocks * p.splits));
-    hipLaunchKernelGGL((kv4_attention_kernel<D, QP, NT, WR>), grid, dim3(256), 0, s, a, p.row_blocks, p.splits);
+    constexpr int PF = 2, WAVES = D <= 128 && QP == 1 ? (NT == 1 ? 2 : 1) : 1;
+    hipLaunchKernelGGL((kv4_attention_kernel<D, QP, NT, WR, PF, WAVES>), grid, dim3(256), 0, s, a, p.row_blocks, p.splits);
     if (p.splits > 1)
         hipLaunchKernelGGL((kv4_join_kernel<D, QP>), dim3((unsigned)((long long)a.c.B * a.c.Hk * a.T * a.G)), dim3(256),
                            0, s, a, p.splits);

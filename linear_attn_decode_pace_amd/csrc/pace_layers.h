@@ -47,6 +47,10 @@ struct Kv4View {
     uint8_t *pool;
     const int32_t *table;   // [B, max_pages]
     int B, Hk, d, page_tokens, n_pages, max_pages;
+    // ceil(2^32 / tiles of a page), or 0 for one tile: the high word of its
+    // product with a tile number is the page's column, exactly for numbers
+    // below 2^27 (cache positions have 31 bits and a page at most 32 tiles)
+    uint32_t per_inv;
 };
 // append: src k / v [T, B, Hk, d]; read: dst float32 (either may be NULL)
 hipError_t launch_kv4_append(const Kv4View &c, const int32_t *start, const int32_t *count, int T,

@@ -64,8 +64,10 @@ int check_heads_q(const pace_kv4_config *cfg, int32_t n_tok) {
 }
 
 Kv4View kv4_view(const pace_kv4_config *cfg, const void *pool, const int32_t *table) {
-    return Kv4View{(uint8_t *)pool, table,           cfg->batch,  cfg->heads_kv,
-                   cfg->d,          cfg->page_tokens, cfg->n_pages, cfg->max_pages};
+    const uint64_t per = cfg->page_tokens / 32;
+    return Kv4View{(uint8_t *)pool, table,           cfg->batch,   cfg->heads_kv,
+                   cfg->d,          cfg->page_tokens, cfg->n_pages, cfg->max_pages,
+                   per == 1 ? 0 : (uint32_t)(((1ull << 32) + per - 1) / per)};
 }
 
 }  // namespace
