@@ -447,6 +447,9 @@ int pace_qk_norm_rope(const pace_norm_config *cfg, const void *q, const void *k,
  *         bytes; may be NULL where that is 0.  Its contents do not matter.
  * All sums and the state are float32.  The chunked kernel splits float32
  * factors into three bf16 parts (24 significant bits) for the matrix cores.
+ * q, k and v of a sequence's tokens, and the state, must be finite: the
+ * chunked form sums over whole chunks of 64 tokens, so a value that is not
+ * reaches earlier tokens of its chunk too.
  * Errors: EINVAL, EUNSUPPORTED, EDEVICE.
  */
 int pace_linear_attn(int32_t batch, int32_t heads, int32_t d_k, int32_t d_v, int32_t n_tok,

@@ -480,9 +480,11 @@ Plan plan_for(const Kv4View &c, int G, int T, int window, int bf16) {
     p.row_blocks = (int)((R + 16 * p.nt * p.wr - 1) / (16 * p.nt * p.wr));
     const long long tiles = ((long long)c.max_pages * c.page_tokens + KV4_TILE - 1) / KV4_TILE;
     const long long groups = (long long)c.B * c.Hk * p.row_blocks;
-    // enough workgroups to fill the card a few times over, but at least four
-    // tiles for each wave
-    const long long want = (4096 + groups - 1) / groups, most = tiles / (4 * (4 / p.wr));
+    // few rows: enough workgroups to fill the card a few times over (lengths
+    // differ), but at least four tiles for each wave.  Many rows: their partial
+    // results cost more than idle units, so only until every unit has work.
+    const long long fill = p.wr == 4 ? 256 : 4096;
+    const long long want = (fill + groups - 1) / groups, most = tiles / (4 * (4 / p.wr));
     p.splits = (int)std::max(1ll, std::min(std::min(want, most), 256ll));
     (void)window;
     return p;

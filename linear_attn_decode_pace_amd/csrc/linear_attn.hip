@@ -1,4 +1,19 @@
-// Linear attention with a fixed decay for each head, recurrent form.
+// Linear attention with a fixed decay g for each head:
+//     M_t = g M_{t-1} + k_t v_t^T,   o_t = scale M_t^T q_t.
+//
+// Recurrent form (decode steps, float32 inputs): the state goes through
+// registers, one read and one write of it bound the step.
+//
+// Chunked form (bf16 prompts): for the tokens i = 0..C-1 of a chunk and the
+// state M before it,
+//     O = diag(g^{i+1}) Q M + (Q K^T o D) V,   D_ij = g^{i-j} for i >= j, else 0,
+//     M <- g^C M + K^T diag(g^{C-1-i}) V,
+// on bf16 matrix cores with float32 sums.  Q, K and V are exact operands; the
+// three float32 factors (M, the weighted scores, the weighted V) are taken in
+// three bf16 parts each, which keep their 24 bits, so outputs and state are as
+// exact as float32 products.
+#include <algorithm>
+
 #include "mfma_common.h"
 #include "pace_layers.h"
 
@@ -75,11 +90,372 @@ hipError_t launch_step(const LinearArgs &a, hipStream_t s) {
     return hipGetLastError();
 }
 
+// ---- chunked form -----------------------------------------------------------
+
+constexpr int LC = 64;   // tokens of a chunk
+
+// Workgroup barrier that orders LDS only: the next chunk's global loads and
+// this one's stores stay in flight across it
+__device__ inline void local_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// g^n from repeated squares in float64
+__device__ inline float power(float g, int n) {
+    double p = 1.0, b = g;
+    for (; n > 0; n >>= 1) {
+        if (n & 1) p *= b;
+        b *= b;
+    }
+    return (float)p;
+}
+
+// eight float32 values as three bf16 operands whose sum has 24 bits
+__device__ inline void split3(float *x, bf16x8 *part) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+        u32x4 w;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            w[e] = pk_bf16(x[2 * e], x[2 * e + 1]);
+            if (i < 2) {
+                x[2 * e] -= lo_f32(w[e]);
+                x[2 * e + 1] -= hi_f32(w[e]);
+            }
+        }
+        part[i] = __builtin_bit_cast(bf16x8, w);
+    }
+}
+
+// 16 x 16 tile of the scores S: place of its probabilities' k-slice (query
+// tile i, slice ks of 32 keys) among the six that are not zero
+__device__ inline int score_slice(int i, int ks) { return i < 2 ? i : 2 * i - 2 + ks; }
+
+enum { LIN_WHOLE, LIN_LOCAL, LIN_OUTPUTS };
+
+// One workgroup: a block of 64 CT columns of one (sequence, head), 16 CT
+// columns for each wave, whose part of M stays in its registers.  All products
+// run over k-slots in the order in which a 16 x 16 accumulator tile leaves
+// its rows in the lanes (slot j of lane group x: row 16 (j / 4) + 4 x + j % 4), so M and
+// the scores are operands as they stand; K^T and V are read from LDS
+// transposed.  Outputs are formed transposed, four adjacent columns of
+// a token in a lane.
+//   LIN_WHOLE: the state from state_in through all tokens to state_out.
+//   LIN_LOCAL: segment `seg` alone, from zero, its state to the workspace.
+//   LIN_OUTPUTS: a segment's outputs from the state before it in the workspace.
+template <int DK, int CT, int MODE>
+__global__ void __launch_bounds__(256, 2) linear_chunk_kernel(LinearArgs a, int col_blocks, int segs, int seg_len) {
+    constexpr int RT = DK / 16, KS = DK / 32, ROW = DK + 8, VROW = 64 * CT + 8;   // rows 4 banks apart
+    constexpr int KP = 64 * (DK / 8) / 256, VP = 2 * CT;                          // 16-byte pieces a thread moves
+    __shared__ uint16_t kx[LC][ROW];
+    __shared__ uint16_t qx[MODE == LIN_LOCAL ? 1 : LC][ROW];
+    __shared__ uint16_t vx[LC][VROW];
+    __shared__ u32x4 px[3][6][MODE == LIN_LOCAL ? 1 : 64];
+    __shared__ float pw[LC + 1], ps[LC + 16];   // g^n; scale g^(n - 15), 0 below n = 15
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n16 = lane & 15, quad = lane >> 4;
+    const int BH = a.B * a.H;
+    const int bh = blockIdx.x % BH, rest = blockIdx.x / BH, cb = rest % col_blocks, seg = rest / col_blocks;
+    const int b = bh / a.H, h = bh - b * a.H;
+    const int len = a.lens ? min(max(a.lens[b], 0), a.T) : a.T;
+    const int lo = seg * seg_len, hi = min(len, lo + seg_len);
+    if (MODE != LIN_WHOLE && lo >= hi) return;
+    const int col0 = cb * 64 * CT + wave * 16 * CT;   // first column of the wave
+    const float g = a.decay[h];
+    for (int i = threadIdx.x; i < LC + 16; i += 256) {
+        const float p = power(g, i - 15 < 0 ? 0 : i - 15);
+        ps[i] = i < 15 ? 0.f : a.scale * p;
+        if (i >= 15) pw[i - 15] = p;
+    }
+
+    f32x4 M[RT][CT];
+    const size_t tile = (size_t)bh * DK * a.dv;
+    const size_t in_state = tile + (size_t)(4 * quad) * a.dv + col0 + n16;
+    const float *from = MODE == LIN_WHOLE ? a.state_in : a.workspace + (size_t)seg * BH * DK * a.dv;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                M[rt][ct][r] = MODE != LIN_LOCAL && from && col0 + 16 * ct < a.dv
+                                   ? from[in_state + (size_t)(16 * rt + r) * a.dv + 16 * ct]
+                                   : 0.f;
+
+    // a thread's 16-byte pieces of a chunk: piece u is row u / (pieces of a row)
+    u32x4 kr[KP], qr[MODE == LIN_LOCAL ? 1 : KP], vr[VP];
+    const size_t kstep = (size_t)BH * DK, vstep = (size_t)BH * a.dv;
+    auto fetch = [&](int c0) {
+#pragma unroll
+        for (int i = 0; i < KP; ++i) {
+            const int u = threadIdx.x + 256 * i, row = u / (DK / 8), at = u % (DK / 8) * 8;
+            const size_t from = (size_t)min(c0 + row, hi - 1) * kstep + (size_t)bh * DK + at;
+            kr[i] = *(const u32x4 *)((const uint16_t *)a.k + from);
+            if constexpr (MODE != LIN_LOCAL) qr[i] = *(const u32x4 *)((const uint16_t *)a.q + from);
+        }
+#pragma unroll
+        for (int i = 0; i < VP; ++i) {
+            const int u = threadIdx.x + 256 * i, row = u / (8 * CT), at = cb * 64 * CT + u % (8 * CT) * 8;
+            const size_t from = (size_t)min(c0 + row, hi - 1) * vstep + (size_t)bh * a.dv + min(at, a.dv - 8);
+            vr[i] = *(const u32x4 *)((const uint16_t *)a.v + from);
+        }
+    };
+    auto put = [&](int c0) {   // rows behind the end become zeros
+        const u32x4 zero = {0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < KP; ++i) {
+            const int u = threadIdx.x + 256 * i, row = u / (DK / 8), at = u % (DK / 8) * 8;
+            const bool ok = c0 + row < hi;
+            *(u32x4 *)&kx[row][at] = ok ? kr[i] : zero;
+            if constexpr (MODE != LIN_LOCAL) *(u32x4 *)&qx[row][at] = ok ? qr[i] : zero;
+        }
+#pragma unroll
+        for (int i = 0; i < VP; ++i) {
+            const int u = threadIdx.x + 256 * i, row = u / (8 * CT), at = u % (8 * CT) * 8;
+            *(u32x4 *)&vx[row][at] = c0 + row < hi && cb * 64 * CT + at < a.dv ? vr[i] : zero;
+        }
+    };
+    // operand of row `row`: k-slots of slice ks, whose elements lie in the row
+    auto row_frag = [&](const uint16_t (*m)[ROW], int row, int ks) {
+        const u32x2 x = *(const u32x2 *)&m[row][32 * ks + 4 * quad], y = *(const u32x2 *)&m[row][32 * ks + 16 + 4 * quad];
+        return __builtin_bit_cast(bf16x8, u32x4{x[0], x[1], y[0], y[1]});
+    };
+    // operand of column c + lane % 16: k-slots are the tokens of slice ks
+    auto col_frag = [&](auto &m, int c, int ks) {
+        typedef __attribute__((address_space(3))) s16x4 *local;
+        s16x4 x[2];
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            x[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((local)&m[32 * ks + 16 * i + 4 * quad + (n16 >> 2)][c + (n16 & 3) * 4]);
+        typedef short s16x8 __attribute__((ext_vector_type(8)));
+        return __builtin_bit_cast(bf16x8, s16x8{x[0][0], x[0][1], x[0][2], x[0][3], x[1][0], x[1][1], x[1][2], x[1][3]});
+    };
+
+    if constexpr (MODE != LIN_LOCAL) {   // halves of the diagonal slices that lie above the diagonal
+        if (wave < 3) {
+            *((u32x2 *)&px[wave][score_slice(0, 0)][lane] + 1) = u32x2{0, 0};
+            *((u32x2 *)&px[wave][score_slice(2, 1)][lane] + 1) = u32x2{0, 0};
+        }
+    }
+    if (lo < hi) {
+        fetch(lo);
+        put(lo);
+    }
+    local_barrier();
+    for (int c0 = lo; c0 < hi; c0 += LC) {
+        const int cl = min(LC, hi - c0);
+        const bool more = c0 + LC < hi;
+        if (more) fetch(c0 + LC);
+        f32x4 o[4][CT];
+        if constexpr (MODE != LIN_LOCAL) {
+            // weighted scores, transposed: tile x of the ten at or below the diagonal
+#pragma unroll
+            for (int it = 0; it < 3; ++it) {
+                const int x = wave + 4 * it;
+                if (x >= 10) break;
+                const int i = x >= 6 ? 3 : x >= 3 ? 2 : x >= 1 ? 1 : 0, j = x - i * (i + 1) / 2;
+                f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks)
+                    s = mfma_bf16_k32(row_frag(kx, 16 * j + n16, ks), row_frag(qx, 16 * i + n16, ks), s);
+                const float *w = ps + 15 + 16 * (i - j) + n16 - 4 * quad;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) s[r] *= w[-r];
+#pragma unroll
+                for (int part = 0; part < 3; ++part) {
+                    const u32x2 p = {pk_bf16(s[0], s[1]), pk_bf16(s[2], s[3])};
+                    *((u32x2 *)&px[part][score_slice(i, j >> 1)][lane] + (j & 1)) = p;
+                    s[0] -= lo_f32(p[0]), s[1] -= hi_f32(p[0]), s[2] -= lo_f32(p[1]), s[3] -= hi_f32(p[1]);
+                }
+            }
+            // Q M
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) o[i][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                bf16x8 m[CT][3];
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) x[e] = M[2 * ks + (e >> 2)][ct][e & 3];
+                    split3(x, m[ct]);
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const bf16x8 qf = row_frag(qx, 16 * i + n16, ks);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                        for (int part = 2; part >= 0; --part) o[i][ct] = mfma_bf16_k32(m[ct][part], qf, o[i][ct]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float w = ps[15 + 16 * i + n16 + 1];
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) o[i][ct] *= w;
+            }
+            local_barrier();   // the scores of all waves are there
+        }
+        bf16x8 vf[2][CT];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct) vf[ks][ct] = col_frag(vx, wave * 16 * CT + 16 * ct, ks);
+        if constexpr (MODE != LIN_LOCAL) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int ks = 0; ks <= i / 2; ++ks)
+#pragma unroll
+                    for (int part = 2; part >= 0; --part) {
+                        const bf16x8 pf = __builtin_bit_cast(bf16x8, px[part][score_slice(i, ks)][lane]);
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) o[i][ct] = mfma_bf16_k32(vf[ks][ct], pf, o[i][ct]);
+                    }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int t = c0 + 16 * i + n16;
+                if (t < hi) {
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+                        if (col0 + 16 * ct < a.dv)
+                            *(f32x4 *)(a.out + (size_t)t * vstep + (size_t)bh * a.dv + col0 + 16 * ct + 4 * quad) = o[i][ct];
+                }
+            }
+        }
+        if (more || MODE != LIN_OUTPUTS) {
+            const float gc = pw[cl];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) M[rt][ct] *= gc;
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                bf16x8 vp[CT][3];
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) {
+                    const u32x4 w = __builtin_bit_cast(u32x4, vf[ks][ct]);
+                    float x[8];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        const int t = 32 * ks + 16 * (e >> 2) + 4 * quad + (e & 3);
+                        x[e] = (e & 1 ? hi_f32(w[e >> 1]) : lo_f32(w[e >> 1])) * pw[max(cl - 1 - t, 0)];
+                    }
+                    split3(x, vp[ct]);
+                }
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const bf16x8 kf = col_frag(kx, 16 * rt, ks);
+#pragma unroll
+                    for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                        for (int part = 2; part >= 0; --part) M[rt][ct] = mfma_bf16_k32(kf, vp[ct][part], M[rt][ct]);
+                }
+            }
+        }
+        if (more) {
+            local_barrier();   // every wave is done with this chunk
+            put(c0 + LC);
+            local_barrier();
+        }
+    }
+    if constexpr (MODE != LIN_OUTPUTS) {
+        float *to = MODE == LIN_WHOLE ? a.state_out : a.workspace + (size_t)seg * BH * DK * a.dv;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (col0 + 16 * ct < a.dv) to[in_state + (size_t)(16 * rt + r) * a.dv + 16 * ct] = M[rt][ct][r];
+    }
+}
+
+// The states before each segment from those that the segments leave alone,
+// in place in the workspace, and the state behind the last token
+__global__ void __launch_bounds__(256) linear_prefix_kernel(LinearArgs a, int segs, int seg_len, int blocks) {
+    const int bh = blockIdx.x / blocks, b = bh / a.H, h = bh - b * a.H;
+    const size_t i = ((size_t)(blockIdx.x - bh * blocks) * 256 + threadIdx.x) * 4, size = (size_t)a.dk * a.dv;
+    if (i >= size) return;
+    const int len = a.lens ? min(max(a.lens[b], 0), a.T) : a.T;
+    const size_t step = (size_t)a.B * a.H * size;
+    float *w = a.workspace + bh * size + i;
+    f32x4 M = a.state_in ? *(const f32x4 *)(a.state_in + bh * size + i) : f32x4{0.f, 0.f, 0.f, 0.f};
+    const float whole = power(a.decay[h], seg_len);
+    const int used = (len + seg_len - 1) / seg_len;
+    constexpr int N = 8;   // segments in flight
+    for (int s0 = 0; s0 < used; s0 += N) {
+        f32x4 x[N];
+#pragma unroll
+        for (int j = 0; j < N; ++j) x[j] = *(const f32x4 *)(w + (size_t)min(s0 + j, used - 1) * step);
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            const int s = s0 + j;
+            if (s >= used) break;
+            *(f32x4 *)(w + (size_t)s * step) = M;
+            const int n = min(len - s * seg_len, seg_len);
+            M = M * (n == seg_len ? whole : power(a.decay[h], n)) + x[j];
+        }
+    }
+    *(f32x4 *)(a.state_out + bh * size + i) = M;
+}
+
+// How a prompt is cut: segments of whole chunks where (sequence, head, column
+// block) alone would leave units idle
+struct LinearPlan {
+    bool chunked;
+    int ct, col_blocks, segs, seg_len;
+};
+LinearPlan linear_plan(int B, int H, int dv, int T, int bf16) {
+    LinearPlan p{bf16 && T > 16, dv <= 64 ? 1 : 2, 1, 1, T};
+    if (!p.chunked) return p;
+    p.col_blocks = (dv + 64 * p.ct - 1) / (64 * p.ct);
+    const long long groups = (long long)B * H * p.col_blocks, chunks = (T + LC - 1) / LC;
+    // a segment reads K and V twice and moves 8 d_k d_v bytes of states: at least
+    // four chunks of it, and only until two workgroups a unit are there
+    const long long want = groups >= 256 ? 1 : 512 / groups;
+    const long long segs = std::max(1ll, std::min(want, chunks / 4));
+    p.seg_len = (int)((chunks + segs - 1) / segs) * LC;
+    p.segs = (T + p.seg_len - 1) / p.seg_len;
+    return p;
+}
+
+template <int DK, int CT>
+void launch_chunks(const LinearArgs &a, const LinearPlan &p, hipStream_t s) {
+    const dim3 grid((unsigned)((long long)a.B * a.H * p.col_blocks * p.segs)), wg(256);
+    if (p.segs == 1) {
+        hipLaunchKernelGGL((linear_chunk_kernel<DK, CT, LIN_WHOLE>), grid, wg, 0, s, a, p.col_blocks, 1, p.seg_len);
+        return;
+    }
+    const int blocks = (a.dk * a.dv / 4 + 255) / 256;
+    hipLaunchKernelGGL((linear_chunk_kernel<DK, CT, LIN_LOCAL>), grid, wg, 0, s, a, p.col_blocks, p.segs, p.seg_len);
+    hipLaunchKernelGGL(linear_prefix_kernel, dim3((unsigned)((long long)a.B * a.H * blocks)), wg, 0, s, a, p.segs,
+                       p.seg_len, blocks);
+    hipLaunchKernelGGL((linear_chunk_kernel<DK, CT, LIN_OUTPUTS>), grid, wg, 0, s, a, p.col_blocks, p.segs, p.seg_len);
+}
+
 }  // namespace
 
-uint64_t linear_attn_workspace(int, int, int, int, int, int) { return 0; }
+uint64_t linear_attn_workspace(int B, int H, int dk, int dv, int T, int bf16) {
+    const LinearPlan p = linear_plan(B, H, dv, T, bf16);
+    return p.segs == 1 ? 0 : (uint64_t)p.segs * B * H * dk * dv * 4;
+}
 
 hipError_t launch_linear_attn(const LinearArgs &a, int bf16, hipStream_t s) {
+    const LinearPlan p = linear_plan(a.B, a.H, a.dv, a.T, bf16);
+    if (p.chunked) {
+        if (a.dk == 128)
+            p.ct == 1 ? launch_chunks<128, 1>(a, p, s) : launch_chunks<128, 2>(a, p, s);
+        else
+            p.ct == 1 ? launch_chunks<64, 1>(a, p, s) : launch_chunks<64, 2>(a, p, s);
+        return hipGetLastError();
+    }
     if (bf16) return a.dk == 128 ? launch_step<uint16_t, 128>(a, s) : launch_step<uint16_t, 64>(a, s);
     return a.dk == 128 ? launch_step<float, 128>(a, s) : launch_step<float, 64>(a, s);
 }
