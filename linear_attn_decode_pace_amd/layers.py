@@ -11,7 +11,7 @@ are all given can be captured into a graph.
 """
 from __future__ import annotations
 
-import contextlib
+import functools
 from typing import Optional, Tuple
 
 import torch
@@ -20,7 +20,10 @@ from . import pace
 
 _DTYPES = {torch.bfloat16: pace.PACE_DTYPE_BF16, torch.float32: pace.PACE_DTYPE_F32}
 _NORMS = {"none": pace.PACE_NORM_NONE, "l2": pace.PACE_NORM_L2, "rms": pace.PACE_NORM_RMS}
-_HERE = contextlib.nullcontext()
+
+# A decode step's calls are shorter than their checks unless those are few
+# Python operations: tensors are compared by device number, and a check's
+# details are worked out only for its message.
 
 
 def _dtype(x: torch.Tensor, name: str) -> int:
@@ -30,72 +33,88 @@ def _dtype(x: torch.Tensor, name: str) -> int:
     return code
 
 
-def _check(x, name: str, dtype, shape, device, dense: bool = True) -> None:
-    """x is a device tensor of this type, shape and device, without gaps."""
+def _refuse(x, name: str, dtype, shape, device: int) -> None:
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
     if not x.is_cuda:
         raise ValueError(f"{name} must be on a GPU, not on {x.device}")
-    if x.device != device:
-        raise ValueError(f"{name} is on {x.device}, the first tensor on {device}")
+    if x.get_device() != device:
+        raise ValueError(f"{name} is on {x.device}, the first tensor on cuda:{device}")
     if x.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, not {x.dtype}")
-    if tuple(x.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(x.shape)}")
-    if dense and not x.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
+    if x.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, not {tuple(x.shape)}")
+    raise ValueError(f"{name} must be contiguous")
 
 
-def _first(x, name: str, dims: int) -> torch.device:
+def _check(x, name: str, dtype, shape: tuple, device: int, dense: bool = True) -> None:
+    """x is a tensor of this type, shape and device, without gaps."""
+    try:
+        if (x.get_device() == device and x.dtype is dtype and x.shape == shape
+                and (not dense or x.is_contiguous())):
+            return
+    except AttributeError:
+        pass
+    _refuse(x, name, dtype, shape, device)
+
+
+def _first(x, name: str, dims: int) -> int:
+    """Number of the device that x, a tensor of so many dimensions, is on."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a tensor")
-    if not x.is_cuda:
+    device = x.get_device()
+    if device < 0:
         raise ValueError(f"{name} must be on a GPU, not on {x.device}")
     if x.dim() != dims:
         raise ValueError(f"{name} must have {dims} dimensions, not {x.dim()}")
-    return x.device
+    return device
 
 
-def _on(device: torch.device, stream):
-    """Context in which `device` is current, and `stream` its current stream."""
+def _elsewhere(device: int, stream):
+    """Context that makes `device` current, and `stream` its current stream;
+    None where that is so already."""
     if stream is not None:
         if not isinstance(stream, torch.cuda.Stream):
             raise TypeError("stream must be a torch.cuda.Stream or None")
-        if stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        if stream.device.index != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{device}")
         return torch.cuda.stream(stream)
-    if torch.cuda.current_device() != device.index:
+    if torch.cuda.current_device() != device:
         return torch.cuda.device(device)
-    return _HERE
+    return None
 
 
-def _workspace(given, need: int, device) -> Tuple[Optional[torch.Tensor], int]:
+# the current stream's handle, without the Stream object around it
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
+                      lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
+def _workspace(given, need: int, like: torch.Tensor) -> Tuple[Optional[torch.Tensor], int]:
     if not need:
         return None, 0
     if given is None:
-        return torch.empty(need, dtype=torch.uint8, device=device), need
+        return like.new_empty(need, dtype=torch.uint8), need
     if not isinstance(given, torch.Tensor) or given.dtype != torch.uint8 or not given.is_contiguous():
         raise TypeError("workspace must be a contiguous uint8 tensor")
-    if given.device != device:
-        raise ValueError(f"workspace is on {given.device}, the tensors on {device}")
+    if given.get_device() != like.get_device():
+        raise ValueError(f"workspace is on {given.device}, the tensors on {like.device}")
     return given, given.numel()
 
 
 # ---- head norms with rotation ----------------------------------------------
 
-def _heads(x, name: str, d: Optional[int]) -> int:
+def _heads(x, name: str, heads: int, d: int) -> int:
     """Row stride of x [tokens, heads, d], whose heads are dense."""
-    if x.dim() != 3:
-        raise ValueError(f"{name} must be [tokens, heads, d]")
-    tokens, heads, dd = x.shape
-    if d is not None and dd != d:
-        raise ValueError(f"{name} has {dd} channels, q has {d}")
-    if (dd > 1 and x.stride(2) != 1) or (heads > 1 and x.stride(1) != dd):
+    if x.is_contiguous():
+        return heads * d
+    row, head, channel = x.stride()
+    if (d > 1 and channel != 1) or (heads > 1 and head != d):
         raise ValueError(f"{name}: the heads of a row must be dense")
-    stride = x.stride(0) if tokens > 1 else heads * dd
-    if stride < heads * dd:
+    if x.shape[0] <= 1:
+        return heads * d
+    if row < heads * d:
         raise ValueError(f"{name}: rows overlap")
-    return stride
+    return row
 
 
 def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None, norm: str = "l2",
@@ -112,12 +131,13 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None, norm: str = 
     device = _first(q, "q", 3)
     code = _dtype(q, "q")
     tokens, hq, d = q.shape
-    q_stride = _heads(q, "q", None)
+    q_stride = _heads(q, "q", hq, d)
     hk = k_stride = 0
     if k is not None:
-        k_stride = _heads(k, "k", d)
+        _first(k, "k", 3)
         hk = k.shape[1]
         _check(k, "k", q.dtype, (tokens, hk, d), device, dense=False)
+        k_stride = _heads(k, "k", hk, d)
     if norm not in _NORMS:
         raise ValueError(f"norm must be one of {sorted(_NORMS)}")
     for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
@@ -132,25 +152,33 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None, norm: str = 
     cfg = pace.pace_norm_config(tokens, hq, hk, d, code, _NORMS[norm], eps, q_scale, rot,
                                 pace.PACE_ROT_ADJACENT if adjacent else pace.PACE_ROT_HALVES,
                                 q_stride, k_stride)
-    with _on(device, stream):
-        if q_out is None:
-            q_out = torch.empty((tokens, hq, d), dtype=q.dtype, device=device)
-        else:
-            _check(q_out, "q_out", q.dtype, (tokens, hq, d), device)
+    if q_out is not None:
+        _check(q_out, "q_out", q.dtype, (tokens, hq, d), device)
+    if k_out is not None:
         if k is None:
-            if k_out is not None:
-                raise ValueError("k_out needs k")
-        elif k_out is None:
-            k_out = torch.empty((tokens, hk, d), dtype=q.dtype, device=device)
-        else:
-            _check(k_out, "k_out", q.dtype, (tokens, hk, d), device)
+            raise ValueError("k_out needs k")
+        _check(k_out, "k_out", q.dtype, (tokens, hk, d), device)
+
+    def call():
+        qo = q.new_empty((tokens, hq, d)) if q_out is None else q_out
+        ko = k.new_empty((tokens, hk, d)) if k_out is None and k is not None else k_out
         if tokens:
             pace.pace_qk_norm_rope(cfg, q, k, q_weight, k_weight, pos if rot else None,
-                                   inv_freq if rot else None, q_out, k_out)
-    return q_out, k_out
+                                   inv_freq if rot else None, qo, ko, _raw_stream(device))
+        return qo, ko
+
+    context = _elsewhere(device, stream)
+    if context is None:
+        return call()
+    with context:
+        return call()
 
 
 # ---- linear attention with a decay for each head ---------------------------
+
+# bytes by sizes alone
+_linear_need = functools.lru_cache(maxsize=256)(pace.pace_linear_attn_workspace)
+
 
 def linear_attention_workspace(q: torch.Tensor, v: torch.Tensor) -> Optional[torch.Tensor]:
     """A workspace for linear_attention calls of these shapes (None if none is needed)."""
@@ -184,20 +212,25 @@ def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: t
         _check(state, "state", torch.float32, (b, h, dk, dv), device)
     if lens is not None:
         _check(lens, "lens", torch.int32, (b,), device)
-    need = pace.pace_linear_attn_workspace(b, h, dk, dv, t, code)
-    with _on(device, stream):
-        if out is None:
-            out = torch.empty((t, b, h, dv), dtype=torch.float32, device=device)
-        else:
-            _check(out, "out", torch.float32, (t, b, h, dv), device)
-        if state_out is None:
-            state_out = torch.empty((b, h, dk, dv), dtype=torch.float32, device=device)
-        else:
-            _check(state_out, "state_out", torch.float32, (b, h, dk, dv), device)
-        ws, n = _workspace(workspace, need, device)
-        pace.pace_linear_attn(b, h, dk, dv, t, code, q, k, v, decay, state_out, out, lens, scale,
-                              state, ws, n)
-    return out, state_out
+    if out is not None:
+        _check(out, "out", torch.float32, (t, b, h, dv), device)
+    if state_out is not None:
+        _check(state_out, "state_out", torch.float32, (b, h, dk, dv), device)
+    need = _linear_need(b, h, dk, dv, t, code)
+
+    def call():
+        o = q.new_empty((t, b, h, dv), dtype=torch.float32) if out is None else out
+        so = q.new_empty((b, h, dk, dv), dtype=torch.float32) if state_out is None else state_out
+        ws, n = _workspace(workspace, need, q)
+        pace.pace_linear_attn(b, h, dk, dv, t, code, q, k, v, decay, so, o, lens, scale, state, ws, n,
+                              _raw_stream(device))
+        return o, so
+
+    context = _elsewhere(device, stream)
+    if context is None:
+        return call()
+    with context:
+        return call()
 
 
 # ---- 4-bit paged KV cache --------------------------------------------------
@@ -217,50 +250,66 @@ class Kv4Cache:
     def nbytes(self) -> int:
         return self.pool.numel()
 
-    def _config(self, table, batch: int, heads_q: int, code: int) -> pace.pace_kv4_config:
-        _first(table, "table", 2)
-        _check(table, "table", torch.int32, (batch, table.shape[1]), self.pool.device)
+    def _config(self, table, batch: int, heads_q: int, code: int) -> Tuple[pace.pace_kv4_config, int]:
+        device = _first(table, "table", 2)
+        if device != self.pool.get_device():
+            raise ValueError(f"table is on {table.device}, the cache on {self.pool.device}")
+        columns = table.shape[1]
+        _check(table, "table", torch.int32, (batch, columns), device)
         return pace.pace_kv4_config(batch, heads_q, self.heads_kv, self.d, self.page_tokens,
-                                    self.pages, table.shape[1], code)
+                                    self.pages, columns, code), device
 
     def append(self, k: torch.Tensor, v: torch.Tensor, table: torch.Tensor, start: torch.Tensor,
                count: Optional[torch.Tensor] = None, stream=None) -> None:
         """Quantize k, v [T, B, heads_kv, d] into positions start[b] + t of the
         cache, for t < count[b] (None: all T).  See pace_kv4_append."""
-        device = self.pool.device
         _first(k, "k", 4)
         t, b = k.shape[0], k.shape[1]
-        cfg = self._config(table, b, 0, _dtype(k, "k"))
-        _check(k, "k", k.dtype, (t, b, self.heads_kv, self.d), device)
-        _check(v, "v", k.dtype, (t, b, self.heads_kv, self.d), device)
+        cfg, device = self._config(table, b, 0, _dtype(k, "k"))
+        shape = (t, b, self.heads_kv, self.d)
+        _check(k, "k", k.dtype, shape, device)
+        _check(v, "v", k.dtype, shape, device)
         _check(start, "start", torch.int32, (b,), device)
         if count is not None:
             _check(count, "count", torch.int32, (b,), device)
-        with _on(device, stream):
-            pace.pace_kv4_append(cfg, self.pool, table, start, t, k, v, count)
+
+        def call():
+            pace.pace_kv4_append(cfg, self.pool, table, start, t, k, v, count, _raw_stream(device))
+
+        context = _elsewhere(device, stream)
+        if context is None:
+            return call()
+        with context:
+            return call()
 
     def read(self, table: torch.Tensor, start: torch.Tensor, n_tok: int,
              count: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
         """float32 (k, v) [n_tok, B, heads_kv, d]: what the cache holds at
         positions start[b] + t (zeros for t >= count[b] and without a page)."""
-        device = self.pool.device
         _first(table, "table", 2)
         b = table.shape[0]
-        cfg = self._config(table, b, 0, pace.PACE_DTYPE_F32)
+        cfg, device = self._config(table, b, 0, pace.PACE_DTYPE_F32)
         _check(start, "start", torch.int32, (b,), device)
         if count is not None:
             _check(count, "count", torch.int32, (b,), device)
         if n_tok < 1:
             raise ValueError("n_tok must be >= 1")
-        with _on(device, stream):
-            k = torch.empty((n_tok, b, self.heads_kv, self.d), dtype=torch.float32, device=device)
-            v = torch.empty_like(k)
-            pace.pace_kv4_read(cfg, self.pool, table, start, n_tok, k, v, count)
-        return k, v
+
+        def call():
+            k = self.pool.new_empty((n_tok, b, self.heads_kv, self.d), dtype=torch.float32)
+            v = self.pool.new_empty((n_tok, b, self.heads_kv, self.d), dtype=torch.float32)
+            pace.pace_kv4_read(cfg, self.pool, table, start, n_tok, k, v, count, _raw_stream(device))
+            return k, v
+
+        context = _elsewhere(device, stream)
+        if context is None:
+            return call()
+        with context:
+            return call()
 
     def attention_workspace(self, q: torch.Tensor, table: torch.Tensor) -> Optional[torch.Tensor]:
         """A workspace for attention calls with queries and tables of these shapes."""
-        cfg = self._config(table, q.shape[1], q.shape[2], _dtype(q, "q"))
+        cfg, _ = self._config(table, q.shape[1], q.shape[2], _dtype(q, "q"))
         need = pace.pace_kv4_attention_workspace(cfg, q.shape[0])
         return torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
 
@@ -273,21 +322,27 @@ class Kv4Cache:
         are the queries' own; window and sinks as in pace_kv4_attention.
         scale defaults to d ** -0.5.  Returns out, of q's type (rows
         t >= count[b] are not written)."""
-        device = _first(q, "q", 4)
+        _first(q, "q", 4)
         t, b, hq, d = q.shape
-        cfg = self._config(table, b, hq, _dtype(q, "q"))
-        _check(q, "q", q.dtype, (t, b, hq, self.d), self.pool.device)
+        cfg, device = self._config(table, b, hq, _dtype(q, "q"))
+        _check(q, "q", q.dtype, (t, b, hq, self.d), device)
         _check(lens, "lens", torch.int32, (b,), device)
         if count is not None:
             _check(count, "count", torch.int32, (b,), device)
+        if out is not None:
+            _check(out, "out", q.dtype, (t, b, hq, d), device)
         need = pace.pace_kv4_attention_workspace(cfg, t)
-        with _on(device, stream):
-            if out is None:
-                out = torch.empty_like(q)
-            else:
-                _check(out, "out", q.dtype, q.shape, device)
-            ws, n = _workspace(workspace, need, device)
-            pace.pace_kv4_attention(cfg, self.pool, table, lens, t, q,
-                                    d ** -0.5 if scale is None else scale, out, count, window, sinks,
-                                    ws, n)
-        return out
+        factor = d ** -0.5 if scale is None else scale
+
+        def call():
+            o = torch.empty_like(q) if out is None else out
+            ws, n = _workspace(workspace, need, q)
+            pace.pace_kv4_attention(cfg, self.pool, table, lens, t, q, factor, o, count, window, sinks,
+                                    ws, n, _raw_stream(device))
+            return o
+
+        context = _elsewhere(device, stream)
+        if context is None:
+            return call()
+        with context:
+            return call()
