@@ -46,15 +46,14 @@ __device__ inline bf16x8 biased_codes(uint32_t w, const CodeBits &k) {
                                             ((w >> 5) & k.mask) | k.one, ((w >> 9) & k.mask) | k.one});
 }
 
-// eight codes of a word as bf16 c, exactly
-__device__ inline bf16x8 exact_codes(uint32_t w, const CodeBits &k) {
-    u32x4 r = __builtin_bit_cast(u32x4, biased_codes(w, k));
-#pragma unroll
-    for (int p = 0; p < 4; ++p) {
-        const uint32_t lo = __float_as_uint(lo_f32(r[p]) - CODE_BIAS), hi = __float_as_uint(hi_f32(r[p]) - CODE_BIAS);
-        r[p] = (lo >> 16) | (hi & 0xffff0000u);
-    }
-    return __builtin_bit_cast(bf16x8, r);
+// eight codes of a word as bf16 c / 16, exactly (see Loader::nibble_f32)
+__device__ inline bf16x8 exact_codes(uint32_t w) {
+    using L = Loader<128, 4>;
+    const uint32_t lo = w ^ 0x88888888u, hi = lo >> 4;   // c + 8 to two's complement
+    return __builtin_bit_cast(bf16x8, u32x4{pk_bf16(L::nibble_f32<0>(lo), L::nibble_f32<2>(lo)),
+                                            pk_bf16(L::nibble_f32<0>(hi), L::nibble_f32<2>(hi)),
+                                            pk_bf16(L::nibble_f32<1>(lo), L::nibble_f32<3>(lo)),
+                                            pk_bf16(L::nibble_f32<1>(hi), L::nibble_f32<3>(hi))});
 }
 
 // max / sum over the four lanes that share lane % 16
@@ -86,19 +85,36 @@ struct TileRegs {
         }
         sc = *(const scales_t *)(tile + 32 * D + lane * (D / 16));
     }
-    __device__ inline uint32_t key_word(int sub, int m) const {
+};
+
+// operands of a tile from its words in registers, with D floats of LDS for its scales
+template <int D, bool EXACT>
+struct RegTile {
+    const TileRegs<D> &t;
+    const float *scales;
+    const CodeBits &bits;
+    __device__ inline bf16x8 codes(uint32_t w) const { return EXACT ? exact_codes(w) : biased_codes(w, bits); }
+    __device__ inline bf16x8 key(int sub, int m, int) const {
         const int w = sub * (D / 32) + m;
-        return k[w >> 2][w & 3];
+        return codes(t.k[w >> 2][w & 3]);
     }
-    __device__ inline uint32_t value_word(int c) const { return v[c >> 2][c & 3]; }
+    __device__ inline bf16x8 value(int c, int) const { return codes(t.v[c >> 2][c & 3]); }
+};
+
+// operands of a tile that its workgroup has unpacked into LDS: [words][64 lanes]
+template <int D>
+struct SharedTile {
+    const bf16x8 *ops;
+    const float *scales;
+    __device__ inline bf16x8 key(int sub, int m, int lane) const { return ops[(sub * (D / 32) + m) * 64 + lane]; }
+    __device__ inline bf16x8 value(int c, int lane) const { return ops[(D / 16 + c) * 64 + lane]; }
 };
 
 // What a workgroup works on: 16 NT rows for each of WR row waves, and 4 / WR
 // waves that share a row wave's tiles.
-template <int D, int QP, int NT, int WR>
+template <int D, int QP, int NT, int WR, bool EXACT>
 struct Attn {
     static constexpr int NG = D / 64, NM = D / 32, NC = D / 16, WK = 4 / WR;
-    static constexpr bool EXACT = QP == 3;
     bf16x8 q[NT][QP][NM];
     f32x4 qoff[NT][NG];
     f32x4 o[NT][NC], psum[NT][NG];
@@ -106,19 +122,82 @@ struct Attn {
     int at[NT];   // last position that the lane's row sees, -1 for none
     float c;
     int window, sinks;
-    CodeBits bits;
-    float *lds;   // the wave's D floats: key scales [group][token], then value scales
 
-    __device__ inline void step(const TileRegs<D> &t, int p0, bool full, int lane) {
-        *(typename TileRegs<D>::scales_t *)(lds + lane * NG) = t.sc;
-        wave_sync();
+    // queries of rows r0 .. as operands, empty sums
+    __device__ inline void init(const Kv4AttnArgs &a, int b, int h, int r0, int len, int n, int lane) {
+        const int n16 = lane & 15, quad = lane >> 4, R = a.T * a.G;
+        window = a.window, sinks = a.sinks;
+        const float sign = a.scale < 0.f ? -1.f : 1.f;
+        this->c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f) * (EXACT ? 16.f : 1.f);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            const int r = r0 + nt * 16 + n16, t = r / a.G;
+            const bool ok = r < R && t < n;
+            at[nt] = ok ? len - n + t : -1;
+            const size_t row = (((size_t)t * a.c.B + b) * a.c.Hk * a.G + (size_t)h * a.G + (r - t * a.G)) * D;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                float sum = 0.f;
+#pragma unroll
+                for (int i = 2 * g; i < 2 * g + 2; ++i) {
+                    const size_t from = row + 32 * i + 8 * quad;
+                    float x[8];
+                    if constexpr (QP == 1) {
+                        u32x4 v = {0, 0, 0, 0};
+                        if (ok) v = *(const u32x4 *)((const uint16_t *)a.q + from);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[2 * e] = lo_f32(v[e]) * sign, x[2 * e + 1] = hi_f32(v[e]) * sign;
+                    } else {
+                        f32x4 v0 = {0.f, 0.f, 0.f, 0.f}, v1 = v0;
+                        if (ok) v0 = *(const f32x4 *)((const float *)a.q + from), v1 = *(const f32x4 *)((const float *)a.q + from + 4);
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) x[e] = v0[e] * sign, x[e + 4] = v1[e] * sign;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) sum += x[e];
+#pragma unroll
+                    for (int part = 0; part < QP; ++part) {
+                        u32x4 v;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            v[e] = pk_bf16(x[2 * e], x[2 * e + 1]);
+                            x[2 * e] -= lo_f32(v[e]);
+                            x[2 * e + 1] -= hi_f32(v[e]);
+                        }
+                        q[nt][part][i] = __builtin_bit_cast(bf16x8, v);
+                    }
+                }
+                const float off = -CODE_BIAS * quad_sum(sum);
+                qoff[nt][g] = f32x4{off, off, off, off};
+                psum[nt][g] = f32x4{0.f, 0.f, 0.f, 0.f};
+            }
+#pragma unroll
+            for (int i = 0; i < NC; ++i) o[nt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
+            m[nt] = -INFINITY, l[nt] = 0.f;
+        }
+    }
+
+    // a row's sums, which its four lanes hold in parts, without the codes' bias
+    __device__ inline void close() {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+            l[nt] = quad_sum(l[nt]);
+#pragma unroll
+            for (int x = 0; x < NC; ++x) o[nt][x] = EXACT ? o[nt][x] * 16.f : o[nt][x] - CODE_BIAS * psum[nt][x >> 2];
+        }
+    }
+
+    // one tile, positions p0 .. p0 + 31; full: every row sees all of them
+    template <class Tile>
+    __device__ inline void step(const Tile &t, int p0, bool full, int lane) {
+        const float *lds = t.scales;   // key scales [group][token], then value scales
         f32x4 sc[NT][2];
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
             bf16x8 ka[NM];
 #pragma unroll
             for (int i = 0; i < NM; ++i)
-                ka[i] = EXACT ? exact_codes(t.key_word(s, i), bits) : biased_codes(t.key_word(s, i), bits);
+                ka[i] = t.key(s, i, lane);
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 const f32x4 ks = *(const f32x4 *)(lds + g * 32 + s * 16 + (lane >> 4) * 4);   // tokens 4 quad ..
@@ -168,8 +247,10 @@ struct Attn {
                 l[nt] *= f;
 #pragma unroll
                 for (int i = 0; i < NC; ++i) o[nt][i] *= f;
+                if constexpr (!EXACT) {
 #pragma unroll
-                for (int g = 0; g < NG; ++g) psum[nt][g] *= f;
+                    for (int g = 0; g < NG; ++g) psum[nt][g] *= f;
+                }
             }
             const float mm = m[nt] == -INFINITY ? 0.f : m[nt];
             float p[2][4];
@@ -215,13 +296,48 @@ struct Attn {
         }
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
-            const bf16x8 va = EXACT ? exact_codes(t.value_word(i), bits) : biased_codes(t.value_word(i), bits);
+            const bf16x8 va = t.value(i, lane);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
                 for (int part = QP - 1; part >= 0; --part)
                     o[nt][i] = mfma_bf16_k32(va, pb[nt][part][i >> 2], o[nt][i]);
         }
+    }
+};
+
+// Tiles that some of the rows r0 .. r0 + rows - 1 see: those of the sinks, then
+// from the first row's window to the last row's position
+struct TileList {
+    int at_lo, at_hi, n_sink, lo, total;
+    __device__ inline TileList(const Kv4AttnArgs &a, int r0, int rows, int len, int n) {
+        const int t_lo = r0 / a.G, t_hi = min((r0 + rows - 1) / a.G, n - 1);
+        at_lo = len - n + t_lo, at_hi = t_lo <= t_hi ? len - n + t_hi : -1;
+        const int end = at_hi < 0 ? 0 : at_hi / KV4_TILE + 1;
+        n_sink = a.window ? min((int)(((long long)a.sinks + KV4_TILE - 1) / KV4_TILE), end) : 0;
+        lo = a.window ? min(max((int)max((long long)at_lo - a.window + 1, 0ll) / KV4_TILE, n_sink), end) : 0;
+        total = n_sink + end - lo;
+    }
+    __device__ inline int tile(int i) const { return i < n_sink ? i : lo + i - n_sink; }
+};
+
+// Address of a tile of (sequence b, head h), and whether it has a page (the
+// pool's first tile otherwise, which may be loaded).  Table entries come by
+// scalar loads, which do not stand in the tiles' queue.
+template <int D>
+struct TileTable {
+    typedef const __attribute__((address_space(4))) int32_t *scalar_ptr;
+    const Kv4View &c;
+    scalar_ptr table;
+    int h, per_page;
+    __device__ inline TileTable(const Kv4View &c, int b, int h)
+        : c(c), table((scalar_ptr)(uintptr_t)(c.table + (size_t)b * c.max_pages)), h(h),
+          per_page(c.page_tokens / KV4_TILE) {}
+    __device__ inline int page(int tile) const { return table[kv4_column(c, tile)]; }
+    __device__ inline bool live(int page) const { return page >= 0 && page < c.n_pages; }
+    __device__ inline const uint8_t *tile(int page, int tile) const {
+        const size_t at = ((size_t)(uint32_t)page * c.Hk + h) * per_page + (tile - kv4_column(c, tile) * per_page);
+        return c.pool + (live(page) ? at * kv4_tile_bytes(D) : 0);
     }
 };
 
@@ -239,9 +355,33 @@ __device__ inline void store4(void *out, size_t i, f32x4 x) {
         *(f32x4 *)((float *)out + i) = x;
 }
 
+// a wave's rows: the result, or its part of it
+template <int D, int QP, int NT, class A>
+__device__ inline void store_rows(const Kv4AttnArgs &a, const A &w, int b, int h, int r0, int n, int split, int splits,
+                                  int lane) {
+    const int n16 = lane & 15, quad = lane >> 4, R = a.T * a.G, bh = b * a.c.Hk + h;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+        const int r = r0 + nt * 16 + n16, t = r / a.G;
+        if (r >= R || t >= n) continue;
+        if (splits == 1) {
+            const float inv = w.l[nt] > 0.f ? 1.f / w.l[nt] : 0.f;
+            const size_t at = (((size_t)t * a.c.B * a.c.Hk + bh) * a.G + (r - t * a.G)) * D;
+#pragma unroll
+            for (int x = 0; x < A::NC; ++x) store4<QP>(a.out, at + 16 * x + 4 * quad, w.o[nt][x] * inv);
+        } else {
+            float *p = partial_row(a, D, split, bh, r);
+#pragma unroll
+            for (int x = 0; x < A::NC; ++x) *(f32x4 *)(p + 16 * x + 4 * quad) = w.o[nt][x];
+            if (quad == 0) *(f32x2 *)(p + D) = f32x2{w.m[nt], w.l[nt]};
+        }
+    }
+}
+
 template <int D, int QP, int NT, int WR, int PF, int WAVES>
 __global__ void __launch_bounds__(256, WAVES) kv4_attention_kernel(Kv4AttnArgs a, int row_blocks, int splits) {
-    using A = Attn<D, QP, NT, WR>;
+    constexpr bool EXACT = QP == 3;
+    using A = Attn<D, QP, NT, WR, EXACT>;
     constexpr int ROWS = 16 * NT * WR, LDW = D + 4;
     __shared__ float scales[4][D];
     const Kv4View &c = a.c;
@@ -261,73 +401,15 @@ __global__ void __launch_bounds__(256, WAVES) kv4_attention_kernel(Kv4AttnArgs a
     const int r0 = rb * ROWS + wr * 16 * NT;
 
     A w;
-    w.window = a.window, w.sinks = a.sinks, w.lds = scales[wave];
-    const float sign = a.scale < 0.f ? -1.f : 1.f;
-    w.c = fmaxf(fabsf(a.scale) * 1.4426950408889634f, 1e-30f);
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        const int r = r0 + nt * 16 + n16, t = r / a.G;
-        const bool ok = r < R && t < n;
-        w.at[nt] = ok ? len - n + t : -1;
-        const size_t row = (((size_t)t * c.B + b) * c.Hk * a.G + (size_t)h * a.G + (r - t * a.G)) * D;
-#pragma unroll
-        for (int g = 0; g < A::NG; ++g) {
-            float sum = 0.f;
-#pragma unroll
-            for (int i = 2 * g; i < 2 * g + 2; ++i) {
-                const size_t at = row + 32 * i + 8 * quad;
-                float x[8];
-                if constexpr (QP == 1) {
-                    u32x4 v = {0, 0, 0, 0};
-                    if (ok) v = *(const u32x4 *)((const uint16_t *)a.q + at);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[2 * e] = lo_f32(v[e]) * sign, x[2 * e + 1] = hi_f32(v[e]) * sign;
-                } else {
-                    f32x4 v0 = {0.f, 0.f, 0.f, 0.f}, v1 = v0;
-                    if (ok) v0 = *(const f32x4 *)((const float *)a.q + at), v1 = *(const f32x4 *)((const float *)a.q + at + 4);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) x[e] = v0[e] * sign, x[e + 4] = v1[e] * sign;
-                }
-#pragma unroll
-                for (int e = 0; e < 8; ++e) sum += x[e];
-#pragma unroll
-                for (int part = 0; part < QP; ++part) {
-                    u32x4 v;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        v[e] = pk_bf16(x[2 * e], x[2 * e + 1]);
-                        x[2 * e] -= lo_f32(v[e]);
-                        x[2 * e + 1] -= hi_f32(v[e]);
-                    }
-                    w.q[nt][part][i] = __builtin_bit_cast(bf16x8, v);
-                }
-            }
-            const float off = -CODE_BIAS * quad_sum(sum);
-            w.qoff[nt][g] = f32x4{off, off, off, off};
-            w.psum[nt][g] = f32x4{0.f, 0.f, 0.f, 0.f};
-        }
-#pragma unroll
-        for (int i = 0; i < A::NC; ++i) w.o[nt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
-        w.m[nt] = -INFINITY, w.l[nt] = 0.f;
-    }
+    w.init(a, b, h, r0, len, n, lane);
+    const CodeBits bits;
 
-    // tiles that some row of the wave sees: those of the sinks, then from the
-    // first row's window to the last row's position
-    const int t_lo = r0 / a.G, t_hi = min((r0 + 16 * NT - 1) / a.G, n - 1);
-    const int at_lo = len - n + t_lo, at_hi = t_lo <= t_hi ? len - n + t_hi : -1;
-    const int end = at_hi < 0 ? 0 : at_hi / KV4_TILE + 1;
-    const int n_sink = a.window ? min((a.sinks + KV4_TILE - 1) / KV4_TILE, end) : 0;
-    const int lo = a.window ? min(max(max(at_lo - a.window + 1, 0) / KV4_TILE, n_sink), end) : 0;
-    const int total = n_sink + end - lo;
-    const int per = (total + splits - 1) / splits;
-    const int first = min(split * per, total), last = min(first + per, total);
-
-    auto tile_of = [&](int i) { return i < n_sink ? i : lo + i - n_sink; };
-    const int per_page = c.page_tokens / KV4_TILE;
-    // table entries come by scalar loads, which do not stand in the tiles' queue
-    typedef const __attribute__((address_space(4))) int32_t *scalar_ptr;
-    const scalar_ptr table = (scalar_ptr)(uintptr_t)(c.table + (size_t)b * c.max_pages);
-    auto page_of = [&](int tile) { return table[kv4_column(c, tile)]; };
+    const TileList list(a, r0, 16 * NT, len, n);
+    const int at_lo = list.at_lo, at_hi = list.at_hi;
+    const int per = (list.total + splits - 1) / splits;
+    const int first = min(split * per, list.total), last = min(first + per, list.total);
+    auto tile_of = [&](int i) { return list.tile(i); };
+    const TileTable<D> table(c, b, h);
     // PF tiles in flight: while the wave works on one, the loads of the next
     // PF - 1 are under way and the table entry of the one behind them is read
     // (past the last tile, and where a tile has no page, the pool's first tile
@@ -335,14 +417,13 @@ __global__ void __launch_bounds__(256, WAVES) kv4_attention_kernel(Kv4AttnArgs a
     TileRegs<D> buf[PF];
     bool live[PF];
     int i = first + wk, ahead = i;
-    int page = ahead < last ? page_of(tile_of(ahead)) : -1;
+    int page = ahead < last ? table.page(tile_of(ahead)) : -1;
     auto fetch = [&](int j) {   // tile `ahead` into slot j
         const int tile = tile_of(ahead);
-        live[j] = page >= 0 && page < c.n_pages;
-        const size_t at = ((size_t)(uint32_t)page * c.Hk + h) * per_page + (tile - kv4_column(c, tile) * per_page);
-        buf[j].load(c.pool + (live[j] ? at * kv4_tile_bytes(D) : 0), lane);
+        live[j] = table.live(page);
+        buf[j].load(table.tile(page, tile), lane);
         ahead += A::WK;
-        page = ahead < last ? page_of(tile_of(ahead)) : -1;
+        page = ahead < last ? table.page(tile_of(ahead)) : -1;
     };
 #pragma unroll
     for (int j = 0; j < PF - 1; ++j) fetch(j);
@@ -356,40 +437,20 @@ __global__ void __launch_bounds__(256, WAVES) kv4_attention_kernel(Kv4AttnArgs a
             if (!live[j]) continue;
             const bool full = p0 + KV4_TILE - 1 <= at_lo &&
                               (a.window == 0 || p0 > at_hi - a.window || p0 + KV4_TILE <= a.sinks);
+            *(typename TileRegs<D>::scales_t *)(scales[wave] + lane * A::NG) = buf[j].sc;
+            wave_sync();
+            const RegTile<D, EXACT> t{buf[j], scales[wave], bits};
             if (full)
-                w.step(buf[j], p0, true, lane);
+                w.step(t, p0, true, lane);
             else
-                w.step(buf[j], p0, false, lane);
+                w.step(t, p0, false, lane);
         }
     }
 
-    // the four lanes of a row hold its sums in parts
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-        w.l[nt] = quad_sum(w.l[nt]);
-        if constexpr (!A::EXACT) {
-#pragma unroll
-            for (int x = 0; x < A::NC; ++x) w.o[nt][x] -= CODE_BIAS * w.psum[nt][x >> 2];
-        }
-    }
+    w.close();
     const size_t out_row = ((size_t)b * c.Hk + h) * a.G;   // + t * B * Hk * G + head
     if constexpr (A::WK == 1) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const int r = r0 + nt * 16 + n16, t = r / a.G;
-            if (r >= R || t >= n) continue;
-            if (splits == 1) {
-                const float inv = w.l[nt] > 0.f ? 1.f / w.l[nt] : 0.f;
-                const size_t at = ((size_t)t * BH * a.G + out_row + (r - t * a.G)) * D;
-#pragma unroll
-                for (int x = 0; x < A::NC; ++x) store4<QP>(a.out, at + 16 * x + 4 * quad, w.o[nt][x] * inv);
-            } else {
-                float *p = partial_row(a, D, split, bh, r);
-#pragma unroll
-                for (int x = 0; x < A::NC; ++x) *(f32x4 *)(p + 16 * x + 4 * quad) = w.o[nt][x];
-                if (quad == 0) *(f32x2 *)(p + D) = f32x2{w.m[nt], w.l[nt]};
-            }
-        }
+        store_rows<D, QP, NT>(a, w, b, h, r0, n, split, splits, lane);
     } else {
         __shared__ float part[4][16][LDW];
 #pragma unroll
@@ -429,18 +490,111 @@ __global__ void __launch_bounds__(256, WAVES) kv4_attention_kernel(Kv4AttnArgs a
     }
 }
 
-// Joins the splits of one row: wave w takes splits w, w + 4, ...
-template <int D, int QP>
+// Workgroup barrier that orders LDS only: loads of the tiles ahead stay in flight
+__device__ inline void local_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Many rows (blocks of a prompt): four waves of 32 rows unpack each pair of
+// tiles once, into LDS in operand order, and all read it; the next pair's
+// loads and unpacking run beside this one's products.
+template <int D, int NT, int WAVES>
+__global__ void __launch_bounds__(256, WAVES) kv4_block_kernel(Kv4AttnArgs a, int row_blocks, int splits) {
+    constexpr int ROWS = 64 * NT, NW = D / 8;   // operands of a tile
+    constexpr int NL = D / 64;                      // 16-byte loads of a lane for a pair: D / 16 KiB in all
+    using A = Attn<D, 1, NT, 4, true>;
+    __shared__ bf16x8 ops[2][2][NW * 64];
+    __shared__ float scales[2][2][D];
+    const Kv4View &c = a.c;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int BH = c.B * c.Hk, R = a.T * a.G;
+    const int bh = blockIdx.x % BH, rest = blockIdx.x / BH;
+    const int split = rest % splits, rb = row_blocks - 1 - rest / splits;
+    const int b = bh / c.Hk, h = bh - b * c.Hk;
+    const int cap = c.max_pages * c.page_tokens;
+    const int len = min(max(a.lens[b], 0), cap), n = a.count ? min(max(a.count[b], 0), a.T) : a.T;
+    if (rb * ROWS / a.G >= n) return;
+    const int r0 = rb * ROWS + wave * 16 * NT;
+    A w;
+    w.init(a, b, h, r0, len, n, lane);
+
+    const TileList list(a, rb * ROWS, ROWS, len, n), mine(a, r0, 16 * NT, len, n);
+    const int per = ((list.total + splits - 1) / splits + 1) & ~1;
+    const int first = min(split * per, list.total), last = min(first + per, list.total);
+    const TileTable<D> table(c, b, h);
+    u32x4 word[NL];
+    float scale = 0.f;
+    const int st = threadIdx.x / D, sx = threadIdx.x % D;   // a thread's scale: tile of the pair, place
+    int live[2] = {}, next[2] = {};   // whether the pair's tiles have a page
+    auto fetch = [&](int i) {   // tiles i and i + 1 of the list
+        const int t0 = list.tile(i), t1 = list.tile(min(i + 1, last - 1));
+        const int g0 = table.page(t0), g1 = table.page(t1);
+        const uint8_t *p0 = table.tile(g0, t0), *p1 = table.tile(g1, t1);
+        next[0] = table.live(g0), next[1] = i + 1 < last && table.live(g1);
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+            const int x = wave + 4 * j;
+            word[j] = *(const u32x4 *)((x < D / 32 ? p0 : p1) + x % (D / 32) * 1024 + lane * 16);
+        }
+        if (st < 2) scale = ((const float *)((st ? p1 : p0) + 32 * D))[sx];
+    };
+    auto unpack = [&](int buf) {
+#pragma unroll
+        for (int j = 0; j < NL; ++j) {
+            const int x = wave + 4 * j;
+            bf16x8 *to = ops[buf][x / (D / 32)] + x % (D / 32) * 256 + lane;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) to[e * 64] = exact_codes(word[j][e]);
+        }
+        if (st < 2) scales[buf][st][sx] = scale;
+        live[0] = next[0], live[1] = next[1];
+    };
+    if (first < last) {
+        fetch(first);
+        unpack(0);
+    }
+    local_barrier();
+    int buf = 0;
+    for (int i = first; i < last; i += 2, buf ^= 1) {
+        const bool more = i + 2 < last;
+        if (more) fetch(i + 2);
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int tile = list.tile(i + j), p0 = tile * KV4_TILE;
+            // none, without a page, or not one of this wave's rows
+            if (!live[j] || p0 > mine.at_hi || (tile >= mine.n_sink && tile < mine.lo)) continue;
+            const SharedTile<D> t{ops[buf][j], scales[buf][j]};
+            const bool full = p0 + KV4_TILE - 1 <= mine.at_lo &&
+                              (a.window == 0 || p0 > mine.at_hi - a.window || p0 + KV4_TILE <= a.sinks);
+            if (full)
+                w.step(t, p0, true, lane);
+            else
+                w.step(t, p0, false, lane);
+        }
+        if (more) unpack(buf ^ 1);
+        local_barrier();
+    }
+    w.close();
+    store_rows<D, 1, NT>(a, w, b, h, r0, n, split, splits, lane);
+}
+
+// Joins the splits of a row.  W waves take its splits in turn (W = 4: many
+// splits of few rows); W = 1: one wave a row, four rows a workgroup.
+template <int D, int QP, int W>
 __global__ void __launch_bounds__(256) kv4_join_kernel(Kv4AttnArgs a, int splits) {
     constexpr int NL = D / 4;   // lanes that hold a row
-    __shared__ float part[4][D + 4];
-    const int R = a.T * a.G, bh = blockIdx.x / R, r = blockIdx.x - bh * R, t = r / a.G, b = bh / a.c.Hk;
+    __shared__ float part[W == 1 ? 1 : 4][D + 4];
+    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63, R = a.T * a.G;
+    const long long row = W == 1 ? (long long)blockIdx.x * 4 + wave : blockIdx.x;
+    if (row >= (long long)a.c.B * a.c.Hk * R) return;
+    const int bh = (int)(row / R), r = (int)(row - (long long)bh * R), t = r / a.G, b = bh / a.c.Hk;
     const int n = a.count ? min(max(a.count[b], 0), a.T) : a.T;
     if (t >= n) return;
-    const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};
     float top = -INFINITY, l = 0.f;
-    for (int s = wave; s < splits; s += 4) {
+    for (int s = W == 1 ? 0 : wave; s < splits; s += W) {
         const float *p = partial_row(a, D, s, bh, r);
         const f32x2 ml = *(const f32x2 *)(p + D);
         const f32x4 x = lane < NL ? *(const f32x4 *)(p + 4 * lane) : sum;
@@ -451,20 +605,23 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(Kv4AttnArgs a, int splits
         l = l * f0 + ml[1] * f1;
         top = m2;
     }
-    if (lane < NL) *(f32x4 *)&part[wave][4 * lane] = sum;
-    if (lane == 0) part[wave][D] = top, part[wave][D + 1] = l;
-    __syncthreads();
-    if (threadIdx.x >= NL) return;
-    top = fmaxf(fmaxf(part[0][D], part[1][D]), fmaxf(part[2][D], part[3][D]));
-    sum = f32x4{0.f, 0.f, 0.f, 0.f}, l = 0.f;
+    if constexpr (W > 1) {
+        if (lane < NL) *(f32x4 *)&part[wave][4 * lane] = sum;
+        if (lane == 0) part[wave][D] = top, part[wave][D + 1] = l;
+        __syncthreads();
+        if (wave > 0 || lane >= NL) return;
+        top = fmaxf(fmaxf(part[0][D], part[1][D]), fmaxf(part[2][D], part[3][D]));
+        sum = f32x4{0.f, 0.f, 0.f, 0.f}, l = 0.f;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-        const float f = part[k][D] > -INFINITY ? __builtin_amdgcn_exp2f(part[k][D] - top) : 0.f;
-        sum += f * *(const f32x4 *)&part[k][4 * threadIdx.x];
-        l = fmaf(f, part[k][D + 1], l);
+        for (int k = 0; k < 4; ++k) {
+            const float f = part[k][D] > -INFINITY ? __builtin_amdgcn_exp2f(part[k][D] - top) : 0.f;
+            sum += f * *(const f32x4 *)&part[k][4 * lane];
+            l = fmaf(f, part[k][D + 1], l);
+        }
     }
+    if (lane >= NL) return;
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    store4<QP>(a.out, (((size_t)t * a.c.B * a.c.Hk + bh) * a.G + (r - t * a.G)) * D + 4 * threadIdx.x, sum * inv);
+    store4<QP>(a.out, (((size_t)t * a.c.B * a.c.Hk + bh) * a.G + (r - t * a.G)) * D + 4 * lane, sum * inv);
 }
 
 // rows of a workgroup, and the number of parts a row's tokens are split into
@@ -483,7 +640,7 @@ Plan plan_for(const Kv4View &c, int G, int T, int window, int bf16) {
     // few rows: enough workgroups to fill the card a few times over (lengths
     // differ), but at least four tiles for each wave.  Many rows: their partial
     // results cost more than idle units, so only until every unit has work.
-    const long long fill = p.wr == 4 ? 256 : 4096;
+    const long long fill = p.wr == 4 ? 512 : 4096;
     const long long want = (fill + groups - 1) / groups, most = tiles / (4 * (4 / p.wr));
     p.splits = (int)std::max(1ll, std::min(std::min(want, most), 256ll));
     (void)window;
@@ -493,11 +650,17 @@ Plan plan_for(const Kv4View &c, int G, int T, int window, int bf16) {
 template <int D, int QP, int NT, int WR>
 void launch(const Kv4AttnArgs &a, const Plan &p, hipStream_t s) {
     const dim3 grid((unsigned)((long long)a.c.B * a.c.Hk * p.row_blocks * p.splits));
+    if constexpr (NT == 2 && WR == 4) {
+        hipLaunchKernelGGL((kv4_block_kernel<D, 2, 2>), grid, dim3(256), 0, s, a, p.row_blocks, p.splits);
+    } else {
     constexpr int PF = 2, WAVES = D <= 128 && QP == 1 ? (NT == 1 ? 2 : 1) : 1;
     hipLaunchKernelGGL((kv4_attention_kernel<D, QP, NT, WR, PF, WAVES>), grid, dim3(256), 0, s, a, p.row_blocks, p.splits);
-    if (p.splits > 1)
-        hipLaunchKernelGGL((kv4_join_kernel<D, QP>), dim3((unsigned)((long long)a.c.B * a.c.Hk * a.T * a.G)), dim3(256),
-                           0, s, a, p.splits);
+    }
+    const long long rows = (long long)a.c.B * a.c.Hk * a.T * a.G;
+    if (p.splits > 8)
+        hipLaunchKernelGGL((kv4_join_kernel<D, QP, 4>), dim3((unsigned)rows), dim3(256), 0, s, a, p.splits);
+    else if (p.splits > 1)
+        hipLaunchKernelGGL((kv4_join_kernel<D, QP, 1>), dim3((unsigned)((rows + 3) / 4)), dim3(256), 0, s, a, p.splits);
 }
 
 template <int D, int QP>
