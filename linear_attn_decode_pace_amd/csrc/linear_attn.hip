@@ -112,22 +112,33 @@ __device__ inline float power(float g, int n) {
     return (float)p;
 }
 
-// eight float32 values as three bf16 operands whose sum has 24 bits
-__device__ inline void split3(float *x, bf16x8 *part) {
-#pragma unroll
-    for (int i = 0; i < 3; ++i) {
-        u32x4 w;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            w[e] = pk_bf16(x[2 * e], x[2 * e + 1]);
-            if (i < 2) {
-                x[2 * e] -= lo_f32(w[e]);
-                x[2 * e + 1] -= hi_f32(w[e]);
-            }
-        }
-        part[i] = __builtin_bit_cast(bf16x8, w);
+// The pairs (-1, 0) and (0, -1) in bf16, kept in registers: as a literal the
+// second would be taken for the inline constant -1.0 of a float32 operand
+struct Minus {
+    uint32_t lo = 0x0000bf80u, hi = 0xbf800000u;
+    __device__ inline Minus() { asm volatile("" : "+s"(lo), "+s"(hi)); }
+    // x minus the first / second element of the pair w, in one dot product
+    __device__ inline float first(uint32_t w, float x) const {
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), __builtin_bit_cast(bf16x2, lo), x, false);
     }
+    __device__ inline float second(uint32_t w, float x) const {
+        return __builtin_amdgcn_fdot2_f32_bf16(__builtin_bit_cast(bf16x2, w), __builtin_bit_cast(bf16x2, hi), x, false);
+    }
+};
+
+// 2 N float32 values as three lists of bf16 pairs whose sum has 24 bits (the
+// remainders x - bf16(x) are exact)
+template <int N>
+__device__ inline void split3(float *x, uint32_t (*part)[N], const Minus &minus) {
+#pragma unroll
+    for (int i = 0; i < 3; ++i)
+#pragma unroll
+        for (int e = 0; e < N; ++e) {
+            const uint32_t w = part[i][e] = pk_bf16(x[2 * e], x[2 * e + 1]);
+            if (i < 2) x[2 * e] = minus.first(w, x[2 * e]), x[2 * e + 1] = minus.second(w, x[2 * e + 1]);
+        }
 }
+__device__ inline bf16x8 operand(const uint32_t *w) { return __builtin_bit_cast(bf16x8, u32x4{w[0], w[1], w[2], w[3]}); }
 
 // 16 x 16 tile of the scores S: place of its probabilities' k-slice (query
 // tile i, slice ks of 32 keys) among the six that are not zero
@@ -147,13 +158,12 @@ enum { LIN_WHOLE, LIN_LOCAL, LIN_OUTPUTS };
 //   LIN_OUTPUTS: a segment's outputs from the state before it in the workspace.
 template <int DK, int CT, int MODE>
 __global__ void __launch_bounds__(256, 2) linear_chunk_kernel(LinearArgs a, int col_blocks, int segs, int seg_len) {
-    constexpr int RT = DK / 16, KS = DK / 32, ROW = DK + 8, VROW = 64 * CT + 8;   // rows 4 banks apart
-    constexpr int KP = 64 * (DK / 8) / 256, VP = 2 * CT;                          // 16-byte pieces a thread moves
-    __shared__ uint16_t kx[LC][ROW];
-    __shared__ uint16_t qx[MODE == LIN_LOCAL ? 1 : LC][ROW];
-    __shared__ uint16_t vx[LC][VROW];
+    constexpr int RT = DK / 16, KS = DK / 32, CB = 64 * CT;
+    constexpr int KP = 64 * (DK / 8) / 256, VP = 2 * CT;   // 16-byte pieces a thread moves
+    constexpr int ROW = DK + 8, VROW = CB + 8;   // rows 4 banks apart, offsets that fit an instruction
+    __shared__ __align__(16) uint16_t kx[LC][ROW], qx[MODE == LIN_LOCAL ? 1 : LC][ROW], vx[LC][VROW];
     __shared__ u32x4 px[3][6][MODE == LIN_LOCAL ? 1 : 64];
-    __shared__ float pw[LC + 1], ps[LC + 16];   // g^n; scale g^(n - 15), 0 below n = 15
+    __shared__ __align__(16) float rw[LC], ps[LC + 16];   // g^(63 - n); scale g^(n - 15), 0 below n = 15
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n16 = lane & 15, quad = lane >> 4;
     const int BH = a.B * a.H;
@@ -167,8 +177,9 @@ __global__ void __launch_bounds__(256, 2) linear_chunk_kernel(LinearArgs a, int 
     for (int i = threadIdx.x; i < LC + 16; i += 256) {
         const float p = power(g, i - 15 < 0 ? 0 : i - 15);
         ps[i] = i < 15 ? 0.f : a.scale * p;
-        if (i >= 15) pw[i - 15] = p;
+        if (i >= 15 && i < 15 + LC) rw[LC - 1 - (i - 15)] = p;
     }
+    const Minus minus;
 
     f32x4 M[RT][CT];
     const size_t tile = (size_t)bh * DK * a.dv;
@@ -184,38 +195,58 @@ __global__ void __launch_bounds__(256, 2) linear_chunk_kernel(LinearArgs a, int 
                                    ? from[in_state + (size_t)(16 * rt + r) * a.dv + 16 * ct]
                                    : 0.f;
 
-    // a thread's 16-byte pieces of a chunk: piece u is row u / (pieces of a row)
+    // A chunk's tokens fill rows 64 - cl .. 63 of LDS: weights then depend on
+    // the row alone, and a chunk of fewer tokens has zeros in front.  Row 0 is
+    // token r0 = c0 + cl - 64; a thread's 16-byte pieces are 256 apart.
     u32x4 kr[KP], qr[MODE == LIN_LOCAL ? 1 : KP], vr[VP];
     const size_t kstep = (size_t)BH * DK, vstep = (size_t)BH * a.dv;
-    auto fetch = [&](int c0) {
+    constexpr int KROWS = 256 / (DK / 8), VROWS = 256 / (CB / 8);   // rows of a pass over the pieces
+    const int krow = threadIdx.x / (DK / 8), vrow = threadIdx.x / (CB / 8);
+    const int kcol = threadIdx.x % (DK / 8) * 8, vcol = threadIdx.x % (CB / 8) * 8;
+    const uint32_t kat = 2 * ((uint32_t)krow * (uint32_t)kstep + kcol);
+    const int vsrc = min(cb * CB + vcol, a.dv - 8);   // columns behind the last are never stored
+    const uint32_t vat = 2 * ((uint32_t)vrow * (uint32_t)vstep + vsrc);
+    auto fetch = [&](int r0) {
+        if (r0 >= lo) {   // wave-uniform rows and 32-bit places in them
 #pragma unroll
-        for (int i = 0; i < KP; ++i) {
-            const int u = threadIdx.x + 256 * i, row = u / (DK / 8), at = u % (DK / 8) * 8;
-            const size_t from = (size_t)min(c0 + row, hi - 1) * kstep + (size_t)bh * DK + at;
-            kr[i] = *(const u32x4 *)((const uint16_t *)a.k + from);
-            if constexpr (MODE != LIN_LOCAL) qr[i] = *(const u32x4 *)((const uint16_t *)a.q + from);
-        }
+            for (int i = 0; i < KP; ++i) {
+                const size_t row = (size_t)(r0 + KROWS * i) * kstep + (size_t)bh * DK;
+                kr[i] = *(const u32x4 *)at((const uint16_t *)a.k + row, kat);
+                if constexpr (MODE != LIN_LOCAL) qr[i] = *(const u32x4 *)at((const uint16_t *)a.q + row, kat);
+            }
 #pragma unroll
-        for (int i = 0; i < VP; ++i) {
-            const int u = threadIdx.x + 256 * i, row = u / (8 * CT), at = cb * 64 * CT + u % (8 * CT) * 8;
-            const size_t from = (size_t)min(c0 + row, hi - 1) * vstep + (size_t)bh * a.dv + min(at, a.dv - 8);
-            vr[i] = *(const u32x4 *)((const uint16_t *)a.v + from);
+            for (int i = 0; i < VP; ++i)
+                vr[i] = *(const u32x4 *)at((const uint16_t *)a.v + (size_t)(r0 + VROWS * i) * vstep + (size_t)bh * a.dv, vat);
+        } else {          // fewer than 64 tokens in all: the rows in front repeat the first
+#pragma unroll
+            for (int i = 0; i < KP; ++i) {
+                const size_t from = (size_t)max(r0 + KROWS * i + krow, lo) * kstep + (size_t)bh * DK + kcol;
+                kr[i] = *(const u32x4 *)((const uint16_t *)a.k + from);
+                if constexpr (MODE != LIN_LOCAL) qr[i] = *(const u32x4 *)((const uint16_t *)a.q + from);
+            }
+#pragma unroll
+            for (int i = 0; i < VP; ++i)
+                vr[i] = *(const u32x4 *)((const uint16_t *)a.v + (size_t)max(r0 + VROWS * i + vrow, lo) * vstep +
+                                         (size_t)bh * a.dv + vsrc);
         }
     };
-    auto put = [&](int c0) {   // rows behind the end become zeros
-        const u32x4 zero = {0, 0, 0, 0};
+    auto put = [&](int skip) {   // rows below `skip` are zeros
+        if (skip) {
+            const u32x4 zero = {0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < KP; ++i)
+                if (KROWS * i + krow < skip) kr[i] = zero, qr[MODE == LIN_LOCAL ? 0 : i] = zero;
+#pragma unroll
+            for (int i = 0; i < VP; ++i)
+                if (VROWS * i + vrow < skip) vr[i] = zero;
+        }
 #pragma unroll
         for (int i = 0; i < KP; ++i) {
-            const int u = threadIdx.x + 256 * i, row = u / (DK / 8), at = u % (DK / 8) * 8;
-            const bool ok = c0 + row < hi;
-            *(u32x4 *)&kx[row][at] = ok ? kr[i] : zero;
-            if constexpr (MODE != LIN_LOCAL) *(u32x4 *)&qx[row][at] = ok ? qr[i] : zero;
+            *(u32x4 *)&kx[KROWS * i + krow][kcol] = kr[i];
+            if constexpr (MODE != LIN_LOCAL) *(u32x4 *)&qx[KROWS * i + krow][kcol] = qr[i];
         }
 #pragma unroll
-        for (int i = 0; i < VP; ++i) {
-            const int u = threadIdx.x + 256 * i, row = u / (8 * CT), at = u % (8 * CT) * 8;
-            *(u32x4 *)&vx[row][at] = c0 + row < hi && cb * 64 * CT + at < a.dv ? vr[i] : zero;
-        }
+        for (int i = 0; i < VP; ++i) *(u32x4 *)&vx[VROWS * i + vrow][vcol] = vr[i];
     };
     // operand of row `row`: k-slots of slice ks, whose elements lie in the row
     auto row_frag = [&](const uint16_t (*m)[ROW], int row, int ks) {
@@ -227,8 +258,10 @@ __global__ void __launch_bounds__(256, 2) linear_chunk_kernel(LinearArgs a, int 
         typedef __attribute__((address_space(3))) s16x4 *local;
         s16x4 x[2];
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            x[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((local)&m[32 * ks + 16 * i + 4 * quad + (n16 >> 2)][c + (n16 & 3) * 4]);
+        for (int i = 0; i < 2; ++i) {
+            const int row = 32 * ks + 16 * i + 4 * quad + (n16 >> 2);
+            x[i] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((local)&m[row][c + (n16 & 3) * 4]);
+        }
         typedef short s16x8 __attribute__((ext_vector_type(8)));
         return __builtin_bit_cast(bf16x8, s16x8{x[0][0], x[0][1], x[0][2], x[0][3], x[1][0], x[1][1], x[1][2], x[1][3]});
     };
@@ -240,68 +273,86 @@ __global__ void __launch_bounds__(256, 2) linear_chunk_kernel(LinearArgs a, int 
         }
     }
     if (lo < hi) {
-        fetch(lo);
-        put(lo);
+        const int skip = max(LC - (hi - lo), 0);
+        fetch(lo - skip);
+        put(skip);
     }
     local_barrier();
     for (int c0 = lo; c0 < hi; c0 += LC) {
-        const int cl = min(LC, hi - c0);
+        const int cl = min(LC, hi - c0), skip = LC - cl, r0 = c0 - skip;
         const bool more = c0 + LC < hi;
-        if (more) fetch(c0 + LC);
+        const int skip2 = max(LC - (hi - c0 - LC), 0);   // of the next chunk
         f32x4 o[4][CT];
         if constexpr (MODE != LIN_LOCAL) {
-            // weighted scores, transposed: tile x of the ten at or below the diagonal
+            // weighted scores, transposed: tiles wave, wave + 4, wave + 8 of the
+            // ten at or below the diagonal
+            f32x4 sc[3];
+            int si[3], sj[3];
 #pragma unroll
             for (int it = 0; it < 3; ++it) {
-                const int x = wave + 4 * it;
-                if (x >= 10) break;
-                const int i = x >= 6 ? 3 : x >= 3 ? 2 : x >= 1 ? 1 : 0, j = x - i * (i + 1) / 2;
-                f32x4 s = {0.f, 0.f, 0.f, 0.f};
+                const int x = min(wave + 4 * it, 9);
+                si[it] = x >= 6 ? 3 : x >= 3 ? 2 : x >= 1 ? 1 : 0, sj[it] = x - si[it] * (si[it] + 1) / 2;
+                sc[it] = f32x4{0.f, 0.f, 0.f, 0.f};
+            }
 #pragma unroll
-                for (int ks = 0; ks < KS; ++ks)
-                    s = mfma_bf16_k32(row_frag(kx, 16 * j + n16, ks), row_frag(qx, 16 * i + n16, ks), s);
+            for (int ks = 0; ks < KS; ++ks)
+#pragma unroll
+                for (int it = 0; it < 3; ++it)
+                    sc[it] = mfma_bf16_k32(row_frag(kx, 16 * sj[it] + n16, ks), row_frag(qx, 16 * si[it] + n16, ks), sc[it]);
+#pragma unroll
+            for (int it = 0; it < 3; ++it) {
+                if (wave + 4 * it >= 10) break;
+                const int i = si[it], j = sj[it];
+                f32x4 s = sc[it];
                 const float *w = ps + 15 + 16 * (i - j) + n16 - 4 * quad;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) s[r] *= w[-r];
+                float x[4] = {s[0], s[1], s[2], s[3]};
+                uint32_t p[3][2];
+                split3<2>(x, p, minus);
 #pragma unroll
-                for (int part = 0; part < 3; ++part) {
-                    const u32x2 p = {pk_bf16(s[0], s[1]), pk_bf16(s[2], s[3])};
-                    *((u32x2 *)&px[part][score_slice(i, j >> 1)][lane] + (j & 1)) = p;
-                    s[0] -= lo_f32(p[0]), s[1] -= hi_f32(p[0]), s[2] -= lo_f32(p[1]), s[3] -= hi_f32(p[1]);
-                }
+                for (int part = 0; part < 3; ++part)
+                    *((u32x2 *)&px[part][score_slice(i, j >> 1)][lane] + (j & 1)) = u32x2{p[part][0], p[part][1]};
             }
-            // Q M
+            // Q M; the parts outermost, so that no product waits for the one before it
 #pragma unroll
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) o[i][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+            bf16x8 qf[2][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) qf[0][i] = row_frag(qx, 16 * i + n16, 0);
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
-                bf16x8 m[CT][3];
+                if (ks + 1 < KS) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) qf[(ks + 1) & 1][i] = row_frag(qx, 16 * i + n16, ks + 1);
+                }
+                uint32_t m[CT][3][4];
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
                     float x[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) x[e] = M[2 * ks + (e >> 2)][ct][e & 3];
-                    split3(x, m[ct]);
+                    split3<4>(x, m[ct], minus);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const bf16x8 qf = row_frag(qx, 16 * i + n16, ks);
+                for (int part = 2; part >= 0; --part)
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct)
+                    for (int i = 0; i < 4; ++i)
 #pragma unroll
-                        for (int part = 2; part >= 0; --part) o[i][ct] = mfma_bf16_k32(m[ct][part], qf, o[i][ct]);
-                }
+                        for (int ct = 0; ct < CT; ++ct)
+                            o[i][ct] = mfma_bf16_k32(operand(m[ct][part]), qf[ks & 1][i], o[i][ct]);
             }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float w = ps[15 + 16 * i + n16 + 1];
+                const float w = ps[max(16 + 16 * i + n16 - skip, 0)];
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) o[i][ct] *= w;
             }
             local_barrier();   // the scores of all waves are there
         }
+        if (more) fetch(c0 + LC - skip2);   // here, where the products need fewer registers
         bf16x8 vf[2][CT];
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
@@ -309,59 +360,60 @@ __global__ void __launch_bounds__(256, 2) linear_chunk_kernel(LinearArgs a, int 
             for (int ct = 0; ct < CT; ++ct) vf[ks][ct] = col_frag(vx, wave * 16 * CT + 16 * ct, ks);
         if constexpr (MODE != LIN_LOCAL) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-                for (int ks = 0; ks <= i / 2; ++ks)
+                for (int part = 2; part >= 0; --part)
 #pragma unroll
-                    for (int part = 2; part >= 0; --part) {
+                    for (int i = 2 * ks; i < 4; ++i) {
                         const bf16x8 pf = __builtin_bit_cast(bf16x8, px[part][score_slice(i, ks)][lane]);
 #pragma unroll
                         for (int ct = 0; ct < CT; ++ct) o[i][ct] = mfma_bf16_k32(vf[ks][ct], pf, o[i][ct]);
                     }
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const int t = c0 + 16 * i + n16;
-                if (t < hi) {
+                if (16 * i + n16 >= skip) {
 #pragma unroll
                     for (int ct = 0; ct < CT; ++ct)
                         if (col0 + 16 * ct < a.dv)
-                            *(f32x4 *)(a.out + (size_t)t * vstep + (size_t)bh * a.dv + col0 + 16 * ct + 4 * quad) = o[i][ct];
+                            *(f32x4 *)at(a.out + (long long)(r0 + 16 * i) * (long long)vstep + (size_t)bh * a.dv + col0 + 16 * ct,
+                                         4 * ((uint32_t)n16 * (uint32_t)vstep + 4 * quad)) = o[i][ct];
                 }
             }
         }
         if (more || MODE != LIN_OUTPUTS) {
-            const float gc = pw[cl];
+            const float gc = cl == LC ? rw[0] * g : rw[LC - 1 - cl];
 #pragma unroll
             for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) M[rt][ct] *= gc;
 #pragma unroll
             for (int ks = 0; ks < 2; ++ks) {
-                bf16x8 vp[CT][3];
+                uint32_t vp[CT][3][4];
+                const f32x4 w0 = *(const f32x4 *)&rw[32 * ks + 4 * quad], w1 = *(const f32x4 *)&rw[32 * ks + 16 + 4 * quad];
 #pragma unroll
                 for (int ct = 0; ct < CT; ++ct) {
-                    const u32x4 w = __builtin_bit_cast(u32x4, vf[ks][ct]);
+                    const u32x4 v = __builtin_bit_cast(u32x4, vf[ks][ct]);
                     float x[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const int t = 32 * ks + 16 * (e >> 2) + 4 * quad + (e & 3);
-                        x[e] = (e & 1 ? hi_f32(w[e >> 1]) : lo_f32(w[e >> 1])) * pw[max(cl - 1 - t, 0)];
-                    }
-                    split3(x, vp[ct]);
+                    for (int e = 0; e < 8; ++e) x[e] = (e & 1 ? hi_f32(v[e >> 1]) : lo_f32(v[e >> 1])) * (e < 4 ? w0[e] : w1[e & 3]);
+                    split3<4>(x, vp[ct], minus);
                 }
 #pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    const bf16x8 kf = col_frag(kx, 16 * rt, ks);
+                for (int rt = 0; rt < RT; rt += 2) {
+                    const bf16x8 kf[2] = {col_frag(kx, 16 * rt, ks), col_frag(kx, 16 * rt + 16, ks)};
 #pragma unroll
-                    for (int ct = 0; ct < CT; ++ct)
+                    for (int part = 2; part >= 0; --part)
 #pragma unroll
-                        for (int part = 2; part >= 0; --part) M[rt][ct] = mfma_bf16_k32(kf, vp[ct][part], M[rt][ct]);
+                        for (int x = 0; x < 2; ++x)
+#pragma unroll
+                            for (int ct = 0; ct < CT; ++ct)
+                                M[rt + x][ct] = mfma_bf16_k32(kf[x], operand(vp[ct][part]), M[rt + x][ct]);
                 }
             }
         }
         if (more) {
             local_barrier();   // every wave is done with this chunk
-            put(c0 + LC);
+            put(skip2);
             local_barrier();
         }
     }
@@ -412,8 +464,9 @@ struct LinearPlan {
     bool chunked;
     int ct, col_blocks, segs, seg_len;
 };
-LinearPlan linear_plan(int B, int H, int dv, int T, int bf16) {
-    LinearPlan p{bf16 && T > 16, dv <= 64 ? 1 : 2, 1, 1, T};
+LinearPlan linear_plan(int B, int H, int dk, int dv, int T, int bf16) {
+    // (the chunked kernel's offsets within a chunk have 32 bits)
+    LinearPlan p{bf16 && T > 16 && (double)B * H * std::max(dk, dv) * 64 < 4294967296.0, dv <= 64 ? 1 : 2, 1, 1, T};
     if (!p.chunked) return p;
     p.col_blocks = (dv + 64 * p.ct - 1) / (64 * p.ct);
     const long long groups = (long long)B * H * p.col_blocks, chunks = (T + LC - 1) / LC;
@@ -443,12 +496,12 @@ void launch_chunks(const LinearArgs &a, const LinearPlan &p, hipStream_t s) {
 }  // namespace
 
 uint64_t linear_attn_workspace(int B, int H, int dk, int dv, int T, int bf16) {
-    const LinearPlan p = linear_plan(B, H, dv, T, bf16);
+    const LinearPlan p = linear_plan(B, H, dk, dv, T, bf16);
     return p.segs == 1 ? 0 : (uint64_t)p.segs * B * H * dk * dv * 4;
 }
 
 hipError_t launch_linear_attn(const LinearArgs &a, int bf16, hipStream_t s) {
-    const LinearPlan p = linear_plan(a.B, a.H, a.dv, a.T, bf16);
+    const LinearPlan p = linear_plan(a.B, a.H, a.dk, a.dv, a.T, bf16);
     if (p.chunked) {
         if (a.dk == 128)
             p.ct == 1 ? launch_chunks<128, 1>(a, p, s) : launch_chunks<128, 2>(a, p, s);
