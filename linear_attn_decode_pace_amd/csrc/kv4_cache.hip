@@ -5,138 +5,205 @@
 namespace pace {
 namespace {
 
-// eight elements
-template <class T>
-__device__ inline void load8(float *x, const void *p, size_t i) {
-    if constexpr (sizeof(T) == 2) {
-        const u32x4 w = *(const u32x4 *)((const uint16_t *)p + i);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[2 * e] = lo_f32(w[e]), x[2 * e + 1] = hi_f32(w[e]);
-    } else {
-        const f32x4 a = *(const f32x4 *)((const float *)p + i), b = *(const f32x4 *)((const float *)p + i + 4);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = a[e], x[e + 4] = b[e];
+// The part of a call that one workgroup works on: a tile of 32 positions of one
+// (sequence, head).  Its arguments come by scalar loads.
+struct TileWork {
+    int b, h, lo, hi, upto;      // tokens lo .. hi - 1 of the tile are the call's, those below `upto` live
+    long long tile, t0;          // t0: the call's token at the tile's first position
+    __device__ inline TileWork(const Kv4View &c, const int32_t *start, const int32_t *count, int n_tok, int tiles) {
+        typedef const __attribute__((address_space(4))) int32_t *scalar_ptr;
+        const int j = blockIdx.x % tiles, bh = blockIdx.x / tiles;
+        b = bh / c.Hk, h = bh - b * c.Hk;
+        const long long first = ((scalar_ptr)(uintptr_t)start)[b];
+        const int n = count ? min(max(((scalar_ptr)(uintptr_t)count)[b], 0), n_tok) : n_tok;
+        tile = (first >> 5) + j;   // rounds down
+        t0 = tile * KV4_TILE - first;
+        lo = (int)max(-t0, 0ll);
+        hi = (int)min((long long)n_tok - t0, (long long)KV4_TILE);
+        upto = (int)min(max((long long)n - t0, 0ll), (long long)KV4_TILE);
     }
-}
+    __device__ inline uint8_t *address(const Kv4View &c) const {
+        typedef const __attribute__((address_space(4))) int32_t *scalar_ptr;
+        if (tile < 0 || tile >= (1 << 26)) return nullptr;
+        const int per = c.page_tokens / KV4_TILE, col = kv4_column(c, (int)tile);
+        if (col >= c.max_pages) return nullptr;
+        const int page = ((scalar_ptr)(uintptr_t)c.table)[(size_t)b * c.max_pages + col];
+        if (page < 0 || page >= c.n_pages) return nullptr;
+        return c.pool + (((size_t)page * c.Hk + h) * per + ((int)tile - col * per)) * kv4_tile_bytes(c.d);
+    }
+};
 
-// Quantize and write.  One workgroup per (sequence, head, tile of 32 tokens),
-// for keys and values in turn; it owns the tile's words, so value words that
-// hold older tokens too are read, changed and written without a race.  Eight
-// lanes take a token's group, eight channels each: the group's largest value
-// is three lane swaps away, and the eight key codes are a word of the layout.
-// Value words hold eight tokens of a channel and are collected through LDS.
-// Codes are 7 x / max in float32: exact quotients where they can tie (bf16
-// inputs have 8 bits, so a quotient that is not a tie is no nearer to one
-// than 2^-9), rounded half to even.
+// eight elements as they stand in memory, and as floats
+template <class T>
+struct Eight {
+    u32x4 w[sizeof(T) / 2];
+    __device__ inline void load(const void *p, size_t i) {
+        const u32x4 *from = (const u32x4 *)((const T *)p + i);
+        w[0] = from[0];
+        if constexpr (sizeof(T) == 4) w[1] = from[1];
+    }
+    __device__ inline float get(int e) const {
+        if constexpr (sizeof(T) == 4) return __uint_as_float(w[e >> 2][e & 3]);
+        return e & 1 ? hi_f32(w[0][e >> 1]) : lo_f32(w[0][e >> 1]);
+    }
+};
+
+// Quantize and write.  One workgroup per (sequence, head, tile of 32 tokens); it
+// owns the tile's words, so value words that hold older tokens too are read,
+// changed and written without a race.  Eight lanes take a token's group, eight
+// channels each: the group's largest value is three lane swaps away, and the
+// eight key codes are a word of the layout.  Value words hold eight tokens of a
+// channel and are collected through LDS.  A call's time is that of its chain of
+// loads (arguments, table, data), so the data are asked for before the table
+// entry is there, and the old value words before the new ones are known.
+// Codes are 7 x / max in float32, rounded half to even.  bf16 inputs have 8
+// bits, so a quotient above 1/2 that is no tie is at least 2^-14 from one, and a
+// quotient within two roundings is enough where it is exact at the ties: the
+// product with a reciprocal, once corrected by its remainder (the remainder of
+// a tie is exact, so the correction ends on it).  float32 inputs take the
+// correctly rounded division.
 template <class T, int D>
 __global__ void __launch_bounds__(256) kv4_append_kernel(Kv4View c, const int32_t *start, const int32_t *count,
                                                          int n_tok, const void *k, const void *v, int tiles) {
-    constexpr int ROW = D + 4;   // bytes: rows of four-token steps in different banks
+    constexpr int ROW = D + 4, PER = D / 8, STEP = 256 / PER, STEPS = KV4_TILE / STEP;   // lanes of a token; tokens a step
     __shared__ __align__(16) uint8_t codes[KV4_TILE * ROW];
-    const int j = blockIdx.x % tiles, bh = blockIdx.x / tiles, b = bh / c.Hk, h = bh - b * c.Hk;
-    const long long first = start[b];
-    const int n = count ? min(max(count[b], 0), n_tok) : n_tok;
-    const long long base = first >= 0 ? first / KV4_TILE : -((-first + KV4_TILE - 1) / KV4_TILE);
-    const long long tile = base + j, p0 = tile * KV4_TILE;   // first position of the tile
-    if (tile < 0 || tile >= (1 << 26) || p0 >= first + n) return;
-    uint8_t *to = kv4_tile(c, b, h, (int)tile);
-    if (!to) return;
-    const int lo = first > p0 ? (int)(first - p0) : 0;                                   // live tokens of the tile
-    const int hi = first + n < p0 + KV4_TILE ? (int)(first + n - p0) : KV4_TILE;
-    constexpr int PER = D / 8;   // lanes of a token
+    const TileWork w(c, start, count, n_tok, tiles);
+    if (w.lo >= w.upto) return;
+    const int t_in = threadIdx.x / PER, ch = threadIdx.x % PER * 8;
+    Eight<T> x[2][STEPS];
 #pragma unroll
-    for (int what = 0; what < 2; ++what) {
-        const void *src = what ? v : k;
-        float *scales = (float *)(to + (what ? kv4_value_scales(D) : kv4_key_scales(D)));
-        // the tokens from lo on, in whole steps of 256 / PER
-        for (int t0 = lo; t0 < hi; t0 += 256 / PER) {
-            const int t = t0 + threadIdx.x / PER, ch = threadIdx.x % PER * 8;
-            const bool live = t < hi;
-            float x[8] = {};
-            if (live) load8<T>(x, src, (((size_t)(p0 + t - first) * c.B + b) * c.Hk + h) * D + ch);
+    for (int s = 0; s < STEPS; ++s) {
+        const int t = s * STEP + t_in;
+        if (t < w.lo || t >= w.upto) continue;
+        const size_t at = (((size_t)(w.t0 + t) * c.B + w.b) * c.Hk + w.h) * D + ch;
+        x[0][s].load(k, at);
+        x[1][s].load(v, at);
+    }
+    uint8_t *to = w.address(c);
+    if (!to) return;
+    // thread i < D packs the four value words at byte 16 i: channels 64 (i / 64) +
+    // 16 e + i % 16, e = 0..3, tokens of lane group (i / 16) % 4
+    u32x4 *words = (u32x4 *)(to + 16 * D) + threadIdx.x;
+    const bool packs = threadIdx.x < D;
+    u32x4 old = {0, 0, 0, 0};
+    if (packs && (w.lo > 0 || w.upto < KV4_TILE)) old = *words;
+#pragma unroll
+    for (int s = 0; s < STEPS; ++s) {
+        const int t = s * STEP + t_in;
+        const bool live = t >= w.lo && t < w.upto;   // the lanes of a group agree
+        if (!live) continue;
+#pragma unroll
+        for (int what = 0; what < 2; ++what) {
             float top = 0.f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[e]));
+            for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[what][s].get(e)));
 #pragma unroll
             for (int m = 1; m < 8; m <<= 1) top = xor_max(top, m);
             uint32_t y[8];
+            if (sizeof(T) == 2 && top > 1e-30f && top < 1e30f) {   // the reciprocal is a normal number
+                const float r = __builtin_amdgcn_rcpf(top);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = (uint32_t)((int)(top > 0.f ? rintf((x[e] * 7.f) / top) : 0.f) + 8);
-            if (!live) continue;
+                for (int e = 0; e < 8; ++e) {
+                    const float x7 = x[what][s].get(e) * 7.f, q = x7 * r;
+                    y[e] = (uint32_t)((int)rintf(fmaf(fmaf(-q, top, x7), r, q)) + 8);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    y[e] = (uint32_t)((int)(top > 0.f ? rintf((x[what][s].get(e) * 7.f) / top) : 0.f) + 8);
+            }
+            float *scales = (float *)(to + (what ? kv4_value_scales(D) : kv4_key_scales(D)));
             if ((threadIdx.x & 7) == 0) scales[ch / KV4_GROUP * KV4_TILE + t] = top / 7.f;
             if (what == 0) {
-                uint32_t w = 0;
+                uint32_t word = 0;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) w |= y[e] << (4 * ((e & 1) * 4 + (e >> 1)));
+                for (int e = 0; e < 8; ++e) word |= y[e] << (4 * ((e & 1) * 4 + (e >> 1)));
                 int nibble;
-                *(uint32_t *)(to + kv4_key_word(D, t, ch, &nibble)) = w;
-            } else {
-                u32x2 w;
-                w[0] = y[0] | y[1] << 8 | y[2] << 16 | y[3] << 24;
-                w[1] = y[4] | y[5] << 8 | y[6] << 16 | y[7] << 24;
-                *(uint32_t *)(codes + t * ROW + ch) = w[0];
-                *(uint32_t *)(codes + t * ROW + ch + 4) = w[1];
+                *(uint32_t *)(to + kv4_key_word(D, t, ch, &nibble)) = word;
+            } else {   // the four channels of a packing thread side by side
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    codes[t * ROW + (ch & ~63) + ((ch + e) & 15) * 4 + ((ch >> 4) & 3)] = (uint8_t)y[e];
             }
         }
     }
     __syncthreads();
-    // value words: four channels of eight tokens at a time, 4 x 8 bytes to 4 words
-    for (int i = threadIdx.x; i < D; i += 256) {
-        const int quad = i / (D / 4), ch = i % (D / 4) * 4;   // tokens 4 quad .. and 16 + 4 quad ..
-        uint32_t w[4] = {}, mask = 0;
+    if (!packs) return;
+    const int quad = (threadIdx.x >> 4) & 3, at = (threadIdx.x & ~63) + (threadIdx.x & 15) * 4;
+    u32x4 word = {0, 0, 0, 0};
+    uint32_t mask = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int t = (e >> 2) * 16 + quad * 4 + (e & 3);
-            if (t < lo || t >= hi) continue;
-            const uint32_t y = *(const uint32_t *)(codes + t * ROW + ch);
-            mask |= 15u << (4 * e);
+    for (int e = 0; e < 8; ++e) {
+        const int t = (e >> 2) * 16 + quad * 4 + (e & 3);
+        if (t < w.lo || t >= w.upto) continue;
+        const uint32_t y = *(const uint32_t *)(codes + t * ROW + at);
+        mask |= 15u << (4 * e);
 #pragma unroll
-            for (int x = 0; x < 4; ++x) w[x] |= ((y >> (8 * x)) & 15u) << (4 * e);
+        for (int i = 0; i < 4; ++i) word[i] |= ((y >> (8 * i)) & 15u) << (4 * e);
+    }
+    if (!mask) return;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) word[i] |= old[i] & ~mask;
+    *words = word;
+}
+
+// Read back: one workgroup per tile, thread i < D takes the 16 bytes of key codes
+// and of value codes at byte 16 i
+template <int D>
+__global__ void __launch_bounds__(D) kv4_read_kernel(Kv4View c, const int32_t *start, const int32_t *count,
+                                                     int n_tok, float *k, float *v, int tiles) {
+    const TileWork w(c, start, count, n_tok, tiles);
+    if (w.lo >= w.hi) return;
+    const uint8_t *tile = w.upto > w.lo ? w.address(c) : nullptr;
+    const int lane = threadIdx.x & 63, group = threadIdx.x >> 6, n16 = lane & 15, quad = lane >> 4;
+    const size_t row = (size_t)c.B * c.Hk * D, base = ((size_t)w.b * c.Hk + w.h) * D;
+    if (k) {
+        u32x4 words = {0, 0, 0, 0};
+        if (tile) words = ((const u32x4 *)tile)[threadIdx.x];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int x = 4 * group + e, t = x / (D / 32) * 16 + n16, ch = x % (D / 32) * 32 + 8 * quad;
+            if (t < w.lo || t >= w.hi) continue;
+            const bool live = tile && t < w.upto;
+            const float s = live ? ((const float *)(tile + kv4_key_scales(D)))[ch / KV4_GROUP * KV4_TILE + t] : 0.f;
+            f32x4 out[2];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int nibble = (i & 1) * 4 + (i >> 1);
+                out[i >> 2][i & 3] = live ? (float)((int)((words[e] >> (4 * nibble)) & 15) - 8) * s : 0.f;
+            }
+            f32x4 *to = (f32x4 *)(k + (size_t)(w.t0 + t) * row + base + ch);
+            to[0] = out[0], to[1] = out[1];
         }
-        if (!mask) continue;
+    }
+    if (v) {
+        u32x4 words = {0, 0, 0, 0};
+        f32x4 s[2] = {};
+        if (tile) {
+            words = ((const u32x4 *)(tile + 16 * D))[threadIdx.x];
+            const float *scales = (const float *)(tile + kv4_value_scales(D)) + group * KV4_TILE + 4 * quad;
+            s[0] = *(const f32x4 *)scales, s[1] = *(const f32x4 *)(scales + 16);
+        }
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            int nibble;
-            uint32_t *dst = (uint32_t *)(to + kv4_value_word(D, quad * 4, ch + x, &nibble));
-            *dst = mask == 0xffffffffu ? w[x] : ((*dst & ~mask) | w[x]);
+        for (int i = 0; i < 8; ++i) {
+            const int t = (i >> 2) * 16 + 4 * quad + (i & 3);
+            if (t < w.lo || t >= w.hi) continue;
+            const bool live = tile && t < w.upto;
+            float *to = v + (size_t)(w.t0 + t) * row + base + 64 * group + n16;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                to[16 * e] = live ? (float)((int)((words[e] >> (4 * i)) & 15) - 8) * s[i >> 2][i & 3] : 0.f;
         }
     }
 }
 
-// Read back: a thread takes four adjacent channels of a token
-__global__ void __launch_bounds__(256) kv4_read_kernel(Kv4View c, const int32_t *start, const int32_t *count,
-                                                       int n_tok, float *k, float *v, long long total) {
-    const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
-    if (i >= total) return;
-    const int per = c.d / 4, ch = (int)(i % per) * 4;
-    const long long row = i / per, bt = row / c.Hk;
-    const int h = (int)(row - bt * c.Hk), t = (int)(bt / c.B), b = (int)(bt - (long long)t * c.B);
-    const long long p = (long long)start[b] + t;
-    const int n = count ? min(max(count[b], 0), n_tok) : n_tok;
-    const uint8_t *tile = t < n && p >= 0 && p < 0x7fffffff ? kv4_tile(c, b, h, (int)(p / KV4_TILE)) : nullptr;
-    f32x4 kx = {0.f, 0.f, 0.f, 0.f}, vx = kx;
-    if (tile) {
-        const int tt = (int)(p % KV4_TILE), g = ch / KV4_GROUP;
-        int nib;
-        const uint32_t wk = *(const uint32_t *)(tile + kv4_key_word(c.d, tt, ch, &nib));
-        const float sk = ((const float *)(tile + kv4_key_scales(c.d)))[g * KV4_TILE + tt];
-        const float sv = ((const float *)(tile + kv4_value_scales(c.d)))[g * KV4_TILE + tt];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int kn = ((e & 1) * 4 + (((ch & 7) + e) >> 1));
-            kx[e] = (float)((int)((wk >> (4 * kn)) & 15) - 8) * sk;
-            const uint32_t wv = *(const uint32_t *)(tile + kv4_value_word(c.d, tt, ch + e, &nib));
-            vx[e] = (float)((int)((wv >> (4 * nib)) & 15) - 8) * sv;
-        }
-    }
-    if (k) *(f32x4 *)(k + 4 * i) = kx;
-    if (v) *(f32x4 *)(v + 4 * i) = vx;
-}
+// most tiles that n tokens touch
+int tiles_of(int n) { return (n + KV4_TILE - 2) / KV4_TILE + 1; }
 
 template <class T>
 void launch_append(const Kv4View &c, const int32_t *start, const int32_t *count, int n_tok, const void *k,
                    const void *v, hipStream_t s) {
-    const int tiles = (n_tok + KV4_TILE - 2) / KV4_TILE + 1;   // most tiles that n_tok tokens touch
+    const int tiles = tiles_of(n_tok);
     const dim3 grid((unsigned)((long long)c.B * c.Hk * tiles)), wg(256);
     if (c.d == 64)
         hipLaunchKernelGGL((kv4_append_kernel<T, 64>), grid, wg, 0, s, c, start, count, n_tok, k, v, tiles);
@@ -156,9 +223,14 @@ hipError_t launch_kv4_append(const Kv4View &c, const int32_t *start, const int32
 
 hipError_t launch_kv4_read(const Kv4View &c, const int32_t *start, const int32_t *count, int T,
                            float *k, float *v, hipStream_t s) {
-    const long long total = (long long)T * c.B * c.Hk * (c.d / 4);
-    hipLaunchKernelGGL(kv4_read_kernel, dim3((unsigned)((total + 255) / 256)), dim3(256), 0, s, c, start, count, T,
-                       k, v, total);
+    const int tiles = tiles_of(T);
+    const dim3 grid((unsigned)((long long)c.B * c.Hk * tiles)), wg((unsigned)c.d);
+    if (c.d == 64)
+        hipLaunchKernelGGL(kv4_read_kernel<64>, grid, wg, 0, s, c, start, count, T, k, v, tiles);
+    else if (c.d == 128)
+        hipLaunchKernelGGL(kv4_read_kernel<128>, grid, wg, 0, s, c, start, count, T, k, v, tiles);
+    else
+        hipLaunchKernelGGL(kv4_read_kernel<256>, grid, wg, 0, s, c, start, count, T, k, v, tiles);
     return hipGetLastError();
 }
 

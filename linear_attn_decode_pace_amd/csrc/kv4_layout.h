@@ -50,14 +50,4 @@ __device__ inline int kv4_column(const Kv4View &c, int tile) {
     return c.per_inv ? (int)__umulhi((uint32_t)tile, c.per_inv) : tile;
 }
 
-// tile `tile` (tokens 32 tile ..) of sequence b, head h; NULL without a page
-__device__ inline uint8_t *kv4_tile(const Kv4View &c, int b, int h, int tile) {
-    if (tile < 0) return nullptr;
-    const int per = c.page_tokens / KV4_TILE, col = kv4_column(c, tile);
-    if (col >= c.max_pages) return nullptr;
-    const int page = c.table[(size_t)b * c.max_pages + col];
-    if (page < 0 || page >= c.n_pages) return nullptr;
-    return c.pool + (((size_t)page * c.Hk + h) * per + (tile - col * per)) * kv4_tile_bytes(c.d);
-}
-
 }  // namespace pace

@@ -587,3 +587,29 @@ def test_wrapper_refusals():
     with pytest.raises(TypeError):
         cache.attention(y, table, n, workspace=torch.empty(1 << 20, device="cuda")) \
             if cache.attention_workspace(y, table) is not None else cache.attention(y, table, n, stream=1)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_cache_codes_are_exact(dtype):
+    """Every pair of a bf16 mantissa and a group's largest value, far apart in size too: codes are those of
+    the exact quotient (its ties are exact in float32), scales within a rounding."""
+    d, page = 64, 32
+    tops = torch.cat([torch.arange(128, 256) * 2.0 ** e for e in (-7, 3, -120, 113)])
+    n = tops.numel() * 4
+    g = ref.gen(31)
+    x = torch.zeros((n, 1, 1, d))
+    for i in range(n):
+        top = tops[i % tops.numel()]
+        m = torch.randint(128, 256, (d,), generator=g) * 2.0 ** torch.randint(-4, 1, (d,), generator=g)
+        v = (m / 255 * top).to(BF16).float() * torch.where(torch.rand(d, generator=g) < 0.5, -1.0, 1.0)
+        v = torch.where(v.abs() > top, top, v)
+        v[i % d] = top
+        if i % 3 == 0:
+            v[(i + 1) % d] = -top / 2           # a tie: 3.5 steps
+        x[i, 0, 0] = v
+    x = x.to(dtype)
+    cache, table = make_cache(1, 1, d, page, (n + page - 1) // page, 5)
+    zero = torch.zeros(1, dtype=torch.int32).cuda()
+    cache.append(x.cuda(), x.cuda(), table.cuda(), zero)
+    for got in cache.read(table.cuda(), zero, n):
+        check_values(got, ref.values(x))
