@@ -121,8 +121,8 @@ __global__ void __launch_bounds__(256) norm_units_kernel(NormArgs a, int L, int 
         else
             c0[j] = 2 * V * u, c1[j] = 2 * V * u + V;
     }
-    const int total = n_tok * a.heads, first = (int)((long long)total * part / splits),
-              last = (int)((long long)total * (part + 1) / splits);
+    const int total = n_tok * a.heads, share = (total + splits - 1) / splits;
+    const int first = part * share, last = min(first + share, total);
     for (int base = first; base < last; base += rows) {
         const int row = base + threadIdx.x / L;
         const bool live = row < last;   // every lane takes part in the sums
@@ -225,11 +225,11 @@ bool try_units(const NormArgs &a, hipStream_t s) {
     while (L < units && L < 64) L *= 2;
     const int U = (units + L - 1) / L;
     if (U > 2) return false;
-    // tokens of a workgroup: several passes of its rows where there are many
+    // tokens of a workgroup: two passes of its rows where there are many
     // tokens (the table of angles is shared by a token's heads), less where
     // that would leave units idle, down to parts of a token
     const int rows = 256 / L;
-    long long per = std::max(1, 4 * rows / a.heads);
+    long long per = std::max(1, 2 * rows / a.heads);
     if (half) per = std::min(per, (long long)std::max(1, 4096 / half));   // 32 KB of angles
     per = std::max(1ll, std::min(per, a.tokens / 1024));
     const long long groups = (a.tokens + per - 1) / per;
