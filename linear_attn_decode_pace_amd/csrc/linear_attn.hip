@@ -471,8 +471,11 @@ LinearPlan linear_plan(int B, int H, int dk, int dv, int T, int bf16) {
     p.col_blocks = (dv + 64 * p.ct - 1) / (64 * p.ct);
     const long long groups = (long long)B * H * p.col_blocks, chunks = (T + LC - 1) / LC;
     // a segment reads K and V twice and moves 8 d_k d_v bytes of states: at least
-    // four chunks of it, and only until two workgroups a unit are there
-    const long long want = groups >= 256 ? 1 : 512 / groups;
+    // four chunks of it, and only until two workgroups a unit are there, or three
+    // where the states are half as large (16 states of 16384 tokens, d_k = 128:
+    // 146 us with 512 workgroups, 172 us with 768 and 165 us with 256; 84 states of up to
+    // 1999 tokens, d_k = 64: 64 us with 512, 55 us with 768)
+    const long long want = groups >= 256 ? 1 : (dk == 64 ? 768 : 512) / groups;
     const long long segs = std::max(1ll, std::min(want, chunks / 4));
     p.seg_len = (int)((chunks + segs - 1) / segs) * LC;
     p.segs = (T + p.seg_len - 1) / p.seg_len;
