@@ -472,8 +472,9 @@ int pace_linear_attn_workspace(int32_t batch, int32_t heads, int32_t d_k, int32_
  * layout is the library's own) and a page table: table[b, i] is the page of
  * sequence b's tokens i * page_tokens ... (i + 1) * page_tokens - 1, or any
  * value outside 0..n_pages - 1 for none: tokens there are not written, read
- * back as zeros and never attended to.  Sequences may share pages to read,
- * but a page that a call writes must belong to one sequence.
+ * back as zeros and never attended to.  Positions that were never written hold
+ * what the pool's memory held.  Sequences may share pages to read, but a page
+ * that a call writes must belong to one sequence.
  */
 #define PACE_KV4_GROUP 64
 

@@ -108,9 +108,10 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(Kv4View c, const int32_
                     y[e] = (uint32_t)((int)rintf(fmaf(fmaf(-q, top, x7), r, q)) + 8);
                 }
             } else {
+                const float f = top > 1e30f ? 0.0625f : 1.f;   // 7 x of the largest values would overflow
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    y[e] = (uint32_t)((int)(top > 0.f ? rintf((x[what][s].get(e) * 7.f) / top) : 0.f) + 8);
+                    y[e] = (uint32_t)((int)(top > 0.f ? rintf((x[what][s].get(e) * f * 7.f) / (top * f)) : 0.f) + 8);
             }
             float *scales = (float *)(to + (what ? kv4_value_scales(D) : kv4_key_scales(D)));
             if ((threadIdx.x & 7) == 0) scales[ch / KV4_GROUP * KV4_TILE + t] = top / 7.f;

@@ -30,6 +30,7 @@ int check_linear(int32_t batch, int32_t heads, int32_t d_k, int32_t d_v, int32_t
     if (rc) return rc;
     if ((rc = check_dtype(in_dtype))) return rc;
     if (n_tok < 1) return fail(PACE_EINVAL, "n_tok must be >= 1");
+    if (n_tok > (1 << 30)) return fail(PACE_EUNSUPPORTED, "n_tok must be at most 2^30");
     if ((double)batch * heads * (d_v / 16) * ((double)n_tok / 64 + 1) > MAX_GRID)
         return fail(PACE_EUNSUPPORTED, "batch * heads * n_tok too large for one call");
     return PACE_OK;

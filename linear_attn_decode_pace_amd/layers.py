@@ -6,8 +6,8 @@ Every computation runs in libpace.so (include/pace.h documents the formulas);
 this module checks tensors, allocates outputs and workspaces with torch, and
 passes pointers.  ``stream`` is a ``torch.cuda.Stream`` or None for the
 current stream of the tensors' device; outputs and workspaces that a call
-allocates belong to that stream.  Nothing here waits, and calls whose buffers
-are all given can be captured into a graph.
+allocates belong to that stream.  Nothing here waits, and every call can be
+captured into a graph.  The calls are for inference: autograd does not see them.
 """
 from __future__ import annotations
 

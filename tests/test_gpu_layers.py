@@ -613,3 +613,78 @@ def test_cache_codes_are_exact(dtype):
     cache.append(x.cuda(), x.cuda(), table.cuda(), zero)
     for got in cache.read(table.cuda(), zero, n):
         check_values(got, ref.values(x))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 1e-38])
+def test_cache_attention_of_unusual_scales(scale, dtype):
+    b, hk, group, t, n, d, page = 2, 2, 3, 7, 150, 128, 64
+    g = ref.gen(17)
+    cache, table = make_cache(b, hk, d, page, 3, 4)
+    k, v = randn((n, b, hk, d), g, BF16), randn((n, b, hk, d), g, BF16)
+    cache.append(k.cuda(), v.cuda(), table.cuda(), torch.zeros(b, dtype=torch.int32).cuda())
+    q = randn((t, b, hk * group, d), g, dtype)
+    lens = torch.tensor([n, 40], dtype=torch.int32)
+    kk, vv = ref.values(k).permute(1, 0, 2, 3), ref.values(v).permute(1, 0, 2, 3)
+    want, mass, reach = ref.attention(q, kk, vv, torch.ones((b, n), dtype=torch.bool), scale, 0, 0, lens, None)
+    got = cache.attention(q.cuda(), table.cuda(), lens.cuda(), scale=scale)
+    check_attention(got.cpu().double(), want, mass, reach, dtype, d, 7.0)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_cache_of_the_largest_and_smallest_values(dtype):
+    """Groups near the largest finite value and of the smallest normal ones.  Scales of the latter are
+    denormal: half a step of 2^-149 for each of up to 7 steps."""
+    d, page, n = 64, 32, 8
+    g = ref.gen(19)
+    x = randn((n, 1, 1, d), g)
+    x = x / x.abs().amax(-1, keepdim=True)
+    size = torch.tensor([3.3e38, 1e38, 3e37, 1e30, 1e-30, 1e-37, 1.2e-38, 1.0])
+    x = (x * size[:, None, None, None]).to(dtype)
+    assert torch.isfinite(x.float()).all()
+    cache, table = make_cache(1, 1, d, page, 1, 5)
+    zero = torch.zeros(1, dtype=torch.int32).cuda()
+    cache.append(x.cuda(), x.cuda(), table.cuda(), zero)
+    want = ref.values(x)
+    for got in cache.read(table.cuda(), zero, n):
+        off = (got.cpu().double() - want).abs()
+        assert (off <= 2.0 ** -23 * want.abs() + 7 * 2.0 ** -149).all()
+
+
+def test_norm_of_keys_alone():
+    """heads_q = 0 through the C entry point."""
+    from linear_attn_decode_pace_amd import pace
+    g = ref.gen(23)
+    k = randn((5, 3, 128), g, BF16)
+    out = torch.empty((5, 3, 128), dtype=BF16, device="cuda")
+    cfg = pace.pace_norm_config(5, 0, 3, 128, pace.PACE_DTYPE_BF16, pace.PACE_NORM_L2, 1e-6, 9.0, 0, 0, 0, 3 * 128)
+    pace.pace_qk_norm_rope(cfg, None, k.cuda(), None, None, None, None, None, out)
+    y = ref.norm_rope(k, "l2", None, 1e-6, None, None, False, 1.0)
+    assert ((out.cpu().double() - y).abs() <= norm_bound(y, BF16, 128)).all()
+
+
+def test_two_calls_at_once():
+    """Calls on two streams with buffers of their own equal the same calls one after another."""
+    g = ref.gen(29)
+    q, k, v, decay, state, _ = linear_inputs(40, 1500, 2, 4, 128, 128, BF16, False, True)
+    one = [x.cuda() for x in (q, k, v, decay, state)]
+    two = [x.cuda() for x in (k, q, v, decay, state * 2)]
+    cache, table = make_cache(4, 2, 128, 64, 40, 3)
+    kk, vv = randn((2500, 4, 2, 128), g, BF16).cuda(), randn((2500, 4, 2, 128), g, BF16).cuda()
+    cache.append(kk, vv, table.cuda(), torch.zeros(4, dtype=torch.int32).cuda())
+    qa, lens = randn((3, 4, 8, 128), g, BF16).cuda(), torch.tensor([2500, 100, 1999, 2048], dtype=torch.int32).cuda()
+    table = table.cuda()
+
+    def calls(x, s):
+        o, e = rt().linear_attention(*x[:4], state=x[4], stream=s)
+        return o, e, cache.attention(qa, table, lens, stream=s)
+
+    want = calls(one, None), calls(two, None)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for s in streams:
+        s.wait_stream(torch.cuda.current_stream())
+    got = [calls(x, s) for x, s in zip((one, two), streams)]
+    torch.cuda.synchronize()
+    for a, c in zip(want, got):
+        assert all(torch.equal(bits(x), bits(y)) for x, y in zip(a, c))
