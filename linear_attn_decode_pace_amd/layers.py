@@ -21,9 +21,16 @@ from . import pace
 _DTYPES = {torch.bfloat16: pace.PACE_DTYPE_BF16, torch.float32: pace.PACE_DTYPE_F32}
 _NORMS = {"none": pace.PACE_NORM_NONE, "l2": pace.PACE_NORM_L2, "rms": pace.PACE_NORM_RMS}
 
-# A decode step's calls are shorter than their checks unless those are few
-# Python operations: tensors are compared by device number, and a check's
-# details are worked out only for its message.
+# A decode step's kernels are shorter than a call's Python unless that is little:
+# tensors are compared by device number, a check's details are worked out only
+# for its message, and pointers go to the C entry points directly (norms of a
+# small batch: 8.3 us a call, of which 2.6 are the launch and 2.3 the outputs'
+# allocation; 9.4 us through the binding's general wrappers).
+_LIB = pace.LIB
+
+
+def _ptr(x: Optional[torch.Tensor]) -> Optional[int]:
+    return None if x is None else x.data_ptr()
 
 
 def _dtype(x: torch.Tensor, name: str) -> int:
@@ -79,19 +86,19 @@ def _elsewhere(device: int, stream):
         if stream.device.index != device:
             raise ValueError(f"stream is on {stream.device}, the tensors on cuda:{device}")
         return torch.cuda.stream(stream)
-    if torch.cuda.current_device() != device:
+    if _current_device() != device:
         return torch.cuda.device(device)
     return None
 
 
-# the current stream's handle, without the Stream object around it
+# the current device's number, and a device's current stream's handle without
+# the Stream object around it (tensors on the device exist: it is initialised)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream",
                       lambda device: torch.cuda.current_stream(device).cuda_stream)
 
 
-def _workspace(given, need: int, like: torch.Tensor) -> Tuple[Optional[torch.Tensor], int]:
-    if not need:
-        return None, 0
+def _workspace(given, need: int, like: torch.Tensor) -> Tuple[torch.Tensor, int]:
     if given is None:
         return like.new_empty(need, dtype=torch.uint8), need
     if not isinstance(given, torch.Tensor) or given.dtype != torch.uint8 or not given.is_contiguous():
@@ -159,19 +166,20 @@ def qk_norm_rope(q: torch.Tensor, k: Optional[torch.Tensor] = None, norm: str = 
             raise ValueError("k_out needs k")
         _check(k_out, "k_out", q.dtype, (tokens, hk, d), device)
 
-    def call():
-        qo = q.new_empty((tokens, hq, d)) if q_out is None else q_out
-        ko = k.new_empty((tokens, hk, d)) if k_out is None and k is not None else k_out
-        if tokens:
-            pace.pace_qk_norm_rope(cfg, q, k, q_weight, k_weight, pos if rot else None,
-                                   inv_freq if rot else None, qo, ko, _raw_stream(device))
-        return qo, ko
-
     context = _elsewhere(device, stream)
-    if context is None:
-        return call()
-    with context:
-        return call()
+    if context is not None:
+        with context:
+            return qk_norm_rope(q, k, norm, q_weight, k_weight, eps, q_scale, pos, inv_freq, adjacent,
+                                q_out, k_out)
+    if q_out is None:
+        q_out = torch.empty_like(q, memory_format=torch.contiguous_format)
+    if k is not None and k_out is None:
+        k_out = torch.empty_like(k, memory_format=torch.contiguous_format)
+    if tokens:
+        pace._check(_LIB.pace_qk_norm_rope(
+            cfg, q.data_ptr(), _ptr(k), _ptr(q_weight), _ptr(k_weight), _ptr(pos) if rot else None,
+            _ptr(inv_freq) if rot else None, q_out.data_ptr(), _ptr(k_out), _raw_stream(device)))
+    return q_out, k_out
 
 
 # ---- linear attention with a decay for each head ---------------------------
@@ -218,22 +226,29 @@ def linear_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, decay: t
         _check(state_out, "state_out", torch.float32, (b, h, dk, dv), device)
     need = _linear_need(b, h, dk, dv, t, code)
 
-    def call():
-        o = q.new_empty((t, b, h, dv), dtype=torch.float32) if out is None else out
-        so = q.new_empty((b, h, dk, dv), dtype=torch.float32) if state_out is None else state_out
-        ws, n = _workspace(workspace, need, q)
-        pace.pace_linear_attn(b, h, dk, dv, t, code, q, k, v, decay, so, o, lens, scale, state, ws, n,
-                              _raw_stream(device))
-        return o, so
-
     context = _elsewhere(device, stream)
-    if context is None:
-        return call()
-    with context:
-        return call()
+    if context is not None:
+        with context:
+            return linear_attention(q, k, v, decay, state, lens, scale, out, state_out, workspace)
+    if out is None:
+        out = v.new_empty((t, b, h, dv), dtype=torch.float32)
+    if state_out is None:
+        state_out = q.new_empty((b, h, dk, dv), dtype=torch.float32) if state is None else torch.empty_like(state)
+    ws, n = _workspace(workspace, need, q) if need else (None, 0)
+    pace._check(_LIB.pace_linear_attn(
+        b, h, dk, dv, t, code, q.data_ptr(), k.data_ptr(), v.data_ptr(), decay.data_ptr(), _ptr(lens), scale,
+        _ptr(state), state_out.data_ptr(), out.data_ptr(), _ptr(ws), n, _raw_stream(device)))
+    return out, state_out
 
 
 # ---- 4-bit paged KV cache --------------------------------------------------
+
+@functools.lru_cache(maxsize=256)
+def _attention_need(batch, heads_q, heads_kv, d, page_tokens, pages, columns, code, t) -> int:
+    """Bytes by sizes alone."""
+    return pace.pace_kv4_attention_workspace(
+        pace.pace_kv4_config(batch, heads_q, heads_kv, d, page_tokens, pages, columns, code), t)
+
 
 class Kv4Cache:
     """The pool of a paged KV cache in 4 bits: `pages` pages of `page_tokens`
@@ -273,14 +288,13 @@ class Kv4Cache:
         if count is not None:
             _check(count, "count", torch.int32, (b,), device)
 
-        def call():
-            pace.pace_kv4_append(cfg, self.pool, table, start, t, k, v, count, _raw_stream(device))
-
         context = _elsewhere(device, stream)
-        if context is None:
-            return call()
-        with context:
-            return call()
+        if context is not None:
+            with context:
+                return self.append(k, v, table, start, count)
+        pace._check(_LIB.pace_kv4_append(
+            cfg, self.pool.data_ptr(), table.data_ptr(), start.data_ptr(), _ptr(count), t, k.data_ptr(),
+            v.data_ptr(), _raw_stream(device)))
 
     def read(self, table: torch.Tensor, start: torch.Tensor, n_tok: int,
              count: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
@@ -295,17 +309,16 @@ class Kv4Cache:
         if n_tok < 1:
             raise ValueError("n_tok must be >= 1")
 
-        def call():
-            k = self.pool.new_empty((n_tok, b, self.heads_kv, self.d), dtype=torch.float32)
-            v = self.pool.new_empty((n_tok, b, self.heads_kv, self.d), dtype=torch.float32)
-            pace.pace_kv4_read(cfg, self.pool, table, start, n_tok, k, v, count, _raw_stream(device))
-            return k, v
-
         context = _elsewhere(device, stream)
-        if context is None:
-            return call()
-        with context:
-            return call()
+        if context is not None:
+            with context:
+                return self.read(table, start, n_tok, count)
+        k = self.pool.new_empty((n_tok, b, self.heads_kv, self.d), dtype=torch.float32)
+        v = torch.empty_like(k)
+        pace._check(_LIB.pace_kv4_read(
+            cfg, self.pool.data_ptr(), table.data_ptr(), start.data_ptr(), _ptr(count), n_tok, k.data_ptr(),
+            v.data_ptr(), _raw_stream(device)))
+        return k, v
 
     def attention_workspace(self, q: torch.Tensor, table: torch.Tensor) -> Optional[torch.Tensor]:
         """A workspace for attention calls with queries and tables of these shapes."""
@@ -331,18 +344,17 @@ class Kv4Cache:
             _check(count, "count", torch.int32, (b,), device)
         if out is not None:
             _check(out, "out", q.dtype, (t, b, hq, d), device)
-        need = pace.pace_kv4_attention_workspace(cfg, t)
-        factor = d ** -0.5 if scale is None else scale
-
-        def call():
-            o = torch.empty_like(q) if out is None else out
-            ws, n = _workspace(workspace, need, q)
-            pace.pace_kv4_attention(cfg, self.pool, table, lens, t, q, factor, o, count, window, sinks,
-                                    ws, n, _raw_stream(device))
-            return o
-
         context = _elsewhere(device, stream)
-        if context is None:
-            return call()
-        with context:
-            return call()
+        if context is not None:
+            with context:
+                return self.attention(q, table, lens, count, scale, window, sinks, out, workspace)
+        need = _attention_need(b, hq, self.heads_kv, self.d, self.page_tokens, self.pages, table.shape[1],
+                               cfg.in_dtype, t)
+        if out is None:
+            out = torch.empty_like(q)
+        ws, n = _workspace(workspace, need, q) if need else (None, 0)
+        pace._check(_LIB.pace_kv4_attention(
+            cfg, self.pool.data_ptr(), table.data_ptr(), lens.data_ptr(), _ptr(count), t, q.data_ptr(),
+            d ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(), _ptr(ws), n,
+            _raw_stream(device)))
+        return out
