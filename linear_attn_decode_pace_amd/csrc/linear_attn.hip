@@ -250,7 +250,10 @@ __global__ void __launch_bounds__(256, 2) linear_chunk_kernel(LinearArgs a, int 
     };
     // operand of row `row`: k-slots of slice ks, whose elements lie in the row
     auto row_frag = [&](const uint16_t (*m)[ROW], int row, int ks) {
-        const u32x2 x = *(const u32x2 *)&m[row][32 * ks + 4 * quad], y = *(const u32x2 *)&m[row][32 * ks + 16 + 4 * quad];
+        // volatile: joined into one paired read the two take twice as long (bank
+        // conflicts between the halves)
+        typedef const volatile __attribute__((address_space(3))) u32x2 *local;
+        const u32x2 x = *(local)&m[row][32 * ks + 4 * quad], y = *(local)&m[row][32 * ks + 16 + 4 * quad];
         return __builtin_bit_cast(bf16x8, u32x4{x[0], x[1], y[0], y[1]});
     };
     // operand of column c + lane % 16: k-slots are the tokens of slice ks
@@ -282,32 +285,39 @@ __global__ void __launch_bounds__(256, 2) linear_chunk_kernel(LinearArgs a, int 
         const int cl = min(LC, hi - c0), skip = LC - cl, r0 = c0 - skip;
         const bool more = c0 + LC < hi;
         const int skip2 = max(LC - (hi - c0 - LC), 0);   // of the next chunk
+        if (more) fetch(c0 + LC - skip2);
         f32x4 o[4][CT];
         if constexpr (MODE != LIN_LOCAL) {
-            // weighted scores, transposed: tiles wave, wave + 4, wave + 8 of the
-            // ten at or below the diagonal
+            // weighted scores, transposed: the ten tiles (i, j) at or below the
+            // diagonal, (3, 0..2), (2, 0..2), (1, 0..1) and (0, 0), (3, 3) to the
+            // four waves, so that a wave's tiles share their operands
+            const int i0 = wave == 3 ? 3 : 3 - wave, i2 = wave == 2 ? 0 : i0;
             f32x4 sc[3];
-            int si[3], sj[3];
 #pragma unroll
-            for (int it = 0; it < 3; ++it) {
-                const int x = min(wave + 4 * it, 9);
-                si[it] = x >= 6 ? 3 : x >= 3 ? 2 : x >= 1 ? 1 : 0, sj[it] = x - si[it] * (si[it] + 1) / 2;
-                sc[it] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int it = 0; it < 3; ++it) sc[it] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks) {
+                const bf16x8 q0 = row_frag(qx, 16 * i0 + n16, ks);
+                if (wave == 3) {
+                    sc[0] = mfma_bf16_k32(row_frag(kx, 48 + n16, ks), q0, sc[0]);
+                } else {
+                    const bf16x8 k0 = row_frag(kx, n16, ks);
+                    sc[0] = mfma_bf16_k32(k0, q0, sc[0]);
+                    sc[1] = mfma_bf16_k32(row_frag(kx, 16 + n16, ks), q0, sc[1]);
+                    if (wave == 2)
+                        sc[2] = mfma_bf16_k32(k0, row_frag(qx, n16, ks), sc[2]);
+                    else
+                        sc[2] = mfma_bf16_k32(row_frag(kx, 32 + n16, ks), q0, sc[2]);
+                }
             }
 #pragma unroll
-            for (int ks = 0; ks < KS; ++ks)
-#pragma unroll
-                for (int it = 0; it < 3; ++it)
-                    sc[it] = mfma_bf16_k32(row_frag(kx, 16 * sj[it] + n16, ks), row_frag(qx, 16 * si[it] + n16, ks), sc[it]);
-#pragma unroll
             for (int it = 0; it < 3; ++it) {
-                if (wave + 4 * it >= 10) break;
-                const int i = si[it], j = sj[it];
-                f32x4 s = sc[it];
+                if (wave == 3 && it > 0) break;
+                const int i = it == 2 ? i2 : i0, j = wave == 3 ? 3 : it == 2 && wave == 2 ? 0 : it;
                 const float *w = ps + 15 + 16 * (i - j) + n16 - 4 * quad;
+                float x[4];
 #pragma unroll
-                for (int r = 0; r < 4; ++r) s[r] *= w[-r];
-                float x[4] = {s[0], s[1], s[2], s[3]};
+                for (int r = 0; r < 4; ++r) x[r] = sc[it][r] * w[-r];
                 uint32_t p[3][2];
                 split3<2>(x, p, minus);
 #pragma unroll
@@ -352,7 +362,6 @@ __global__ void __launch_bounds__(256, 2) linear_chunk_kernel(LinearArgs a, int 
             }
             local_barrier();   // the scores of all waves are there
         }
-        if (more) fetch(c0 + LC - skip2);   // here, where the products need fewer registers
         bf16x8 vf[2][CT];
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
