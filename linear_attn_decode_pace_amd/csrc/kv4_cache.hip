@@ -99,26 +99,30 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(Kv4View c, const int32_
             for (int e = 0; e < 8; ++e) top = fmaxf(top, fabsf(x[what][s].get(e)));
 #pragma unroll
             for (int m = 1; m < 8; m <<= 1) top = xor_max(top, m);
+            // codes by the rounding of 1.5 * 2^23 + 8 + quotient: c + 8 in the low
+            // bits of y, above them those of BASE
+            constexpr float MAGIC = 12582912.f + 8.f;
+            constexpr uint32_t BASE = 0x4b400000u;
             uint32_t y[8];
             if (sizeof(T) == 2 && top > 1e-30f && top < 1e30f) {   // the reciprocal is a normal number
                 const float r = __builtin_amdgcn_rcpf(top);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     const float x7 = x[what][s].get(e) * 7.f, q = x7 * r;
-                    y[e] = (uint32_t)((int)rintf(fmaf(fmaf(-q, top, x7), r, q)) + 8);
+                    y[e] = __float_as_uint(fmaf(fmaf(-q, top, x7), r, q) + MAGIC);
                 }
             } else {
                 const float f = top > 1e30f ? 0.0625f : 1.f;   // 7 x of the largest values would overflow
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    y[e] = (uint32_t)((int)(top > 0.f ? rintf((x[what][s].get(e) * f * 7.f) / (top * f)) : 0.f) + 8);
+                    y[e] = __float_as_uint((top > 0.f ? (x[what][s].get(e) * f * 7.f) / (top * f) : 0.f) + MAGIC);
             }
             float *scales = (float *)(to + (what ? kv4_value_scales(D) : kv4_key_scales(D)));
             if ((threadIdx.x & 7) == 0) scales[ch / KV4_GROUP * KV4_TILE + t] = top / 7.f;
             if (what == 0) {
-                uint32_t word = 0;
+                uint32_t word = 0u - BASE * 0x11111111u;   // takes BASE from every place
 #pragma unroll
-                for (int e = 0; e < 8; ++e) word |= y[e] << (4 * ((e & 1) * 4 + (e >> 1)));
+                for (int e = 0; e < 8; ++e) word += y[e] << (4 * ((e & 1) * 4 + (e >> 1)));
                 int nibble;
                 *(uint32_t *)(to + kv4_key_word(D, t, ch, &nibble)) = word;
             } else {   // the four channels of a packing thread side by side
