@@ -12,13 +12,14 @@
 // (kv4_layout.h stores values so): nothing passes through LDS, and the row
 // statistics are a lane's own values plus two lane swaps.
 //
-// Codes.  A nibble n = c + 8 becomes the bf16 16 + n by one shift and one
-// and-or for two codes (exponent 4, n in the upper mantissa bits), so operands
-// hold c + 24.  The constant leaves each product exactly in float32:
-// accumulators of S start at -24 sum(q) of their 64 channels, and O
-// loses 24 sum(p) at the end, with sum(p) of the rounded p from one more
-// product with a tile of ones.  Scales multiply S per token and group, and p
-// per token and group before it is rounded.
+// Codes.  Values become bf16 c / 16, exactly.  Keys, where every wave unpacks
+// for itself, take a cheaper form: a nibble n = c + 8 is the bf16 16 + n by one shift and
+// one and-or for two codes (exponent 4, n in the upper mantissa bits), so operands
+// hold c + 24, and the accumulators of S start at -24 sum(q) of their 64
+// channels.  (Values in that form too, less 24 sum(p) at the end, take 290 us
+// instead of 294 us on 64 caches of up to 32768 tokens, but leave the rounding
+// of the 24 sum(p) in outputs that should be zero.)  Scales multiply S per token
+// and group, and p per token and group before it is rounded.
 //
 // Row maxima are lazy: a wave rescales its sums only where a score exceeds the
 // row's reference by 2^8 or more, which is exact in float32 and keeps the
@@ -93,12 +94,11 @@ struct RegTile {
     const TileRegs<D> &t;
     const float *scales;
     const CodeBits &bits;
-    __device__ inline bf16x8 codes(uint32_t w) const { return EXACT ? exact_codes(w) : biased_codes(w, bits); }
     __device__ inline bf16x8 key(int sub, int m, int) const {
         const int w = sub * (D / 32) + m;
-        return codes(t.k[w >> 2][w & 3]);
+        return EXACT ? exact_codes(t.k[w >> 2][w & 3]) : biased_codes(t.k[w >> 2][w & 3], bits);
     }
-    __device__ inline bf16x8 value(int c, int) const { return codes(t.v[c >> 2][c & 3]); }
+    __device__ inline bf16x8 value(int c, int) const { return exact_codes(t.v[c >> 2][c & 3]); }
 };
 
 // operands of a tile that its workgroup has unpacked into LDS: [words][64 lanes]
@@ -117,7 +117,7 @@ struct Attn {
     static constexpr int NG = D / 64, NM = D / 32, NC = D / 16, WK = 4 / WR;
     bf16x8 q[NT][QP][NM];
     f32x4 qoff[NT][NG];
-    f32x4 o[NT][NC], psum[NT][NG];
+    f32x4 o[NT][NC];
     float m[NT], l[NT];
     int at[NT];   // last position that the lane's row sees, -1 for none
     float c;
@@ -169,7 +169,6 @@ struct Attn {
                 }
                 const float off = -CODE_BIAS * quad_sum(sum);
                 qoff[nt][g] = f32x4{off, off, off, off};
-                psum[nt][g] = f32x4{0.f, 0.f, 0.f, 0.f};
             }
 #pragma unroll
             for (int i = 0; i < NC; ++i) o[nt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -177,13 +176,13 @@ struct Attn {
         }
     }
 
-    // a row's sums, which its four lanes hold in parts, without the codes' bias
+    // a row's sums, which its four lanes hold in parts, in the values' own units
     __device__ inline void close() {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             l[nt] = quad_sum(l[nt]);
 #pragma unroll
-            for (int x = 0; x < NC; ++x) o[nt][x] = EXACT ? o[nt][x] * 16.f : o[nt][x] - CODE_BIAS * psum[nt][x >> 2];
+            for (int x = 0; x < NC; ++x) o[nt][x] *= 16.f;
         }
     }
 
@@ -247,10 +246,6 @@ struct Attn {
                 l[nt] *= f;
 #pragma unroll
                 for (int i = 0; i < NC; ++i) o[nt][i] *= f;
-                if constexpr (!EXACT) {
-#pragma unroll
-                    for (int g = 0; g < NG; ++g) psum[nt][g] *= f;
-                }
             }
             const float mm = m[nt] == -INFINITY ? 0.f : m[nt];
             float p[2][4];
@@ -287,13 +282,6 @@ struct Attn {
             }
         }
         __builtin_amdgcn_sched_barrier(0);
-        if constexpr (!EXACT) {
-            const bf16x8 ones = __builtin_bit_cast(bf16x8, u32x4{0x3f803f80u, 0x3f803f80u, 0x3f803f80u, 0x3f803f80u});
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int g = 0; g < NG; ++g) psum[nt][g] = mfma_bf16_k32(ones, pb[nt][0][g], psum[nt][g]);
-        }
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
             const bf16x8 va = t.value(i, lane);

@@ -688,3 +688,19 @@ def test_two_calls_at_once():
     torch.cuda.synchronize()
     for a, c in zip(want, got):
         assert all(torch.equal(bits(x), bits(y)) for x, y in zip(a, c))
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_cache_channels_of_zeros_stay_zero(dtype):
+    """Value channels that are zero in every token give exactly zero."""
+    b, hk, d, page, n = 2, 2, 128, 64, 700
+    g = ref.gen(37)
+    cache, table = make_cache(b, hk, d, page, 11, 6)
+    k, v = randn((n, b, hk, d), g, BF16), randn((n, b, hk, d), g, BF16)
+    v[..., 5], v[..., 64:] = 0, 0
+    cache.append(k.cuda(), v.cuda(), table.cuda(), torch.zeros(b, dtype=torch.int32).cuda())
+    lens = torch.tensor([n, 3], dtype=torch.int32).cuda()
+    for t in (1, 30):                  # both kernels
+        q = randn((t, b, hk * 4, d), g, dtype).cuda()
+        got = cache.attention(q, table.cuda(), lens)
+        assert (got[..., 5] == 0).all() and (got[..., 64:] == 0).all() and (got[-1, ..., :5] != 0).any()
