@@ -16,9 +16,9 @@
 // for itself, take a cheaper form: a nibble n = c + 8 is the bf16 16 + n by one shift and
 // one and-or for two codes (exponent 4, n in the upper mantissa bits), so operands
 // hold c + 24, and the accumulators of S start at -24 sum(q) of their 64
-// channels.  (Values in that form too, less 24 sum(p) at the end, take 290 us
-// instead of 294 us on 64 caches of up to 32768 tokens, but leave the rounding
-// of the 24 sum(p) in outputs that should be zero.)  Scales multiply S per token
+// channels.  (Values in that form too, less 24 sum(p) at the end, take 1% less
+// time on 64 caches of up to 32768 tokens, but leave the rounding of the
+// 24 sum(p) in outputs that should be zero.)  Scales multiply S per token
 // and group, and p per token and group before it is rounded.
 //
 // Row maxima are lazy: a wave rescales its sums only where a score exceeds the
@@ -47,15 +47,17 @@ __device__ inline bf16x8 biased_codes(uint32_t w, const CodeBits &k) {
                                             ((w >> 5) & k.mask) | k.one, ((w >> 9) & k.mask) | k.one});
 }
 
-// eight codes of a word as bf16 c / 16, exactly (see Loader::nibble_f32)
-__device__ inline bf16x8 exact_codes(uint32_t w) {
+// eight two's complement codes of a word as bf16 c / 16, exactly (see Loader::nibble_f32)
+__device__ inline bf16x8 exact_codes(uint32_t lo) {
     using L = Loader<128, 4>;
-    const uint32_t lo = w ^ 0x88888888u, hi = lo >> 4;   // c + 8 to two's complement
+    const uint32_t hi = lo >> 4;
     return __builtin_bit_cast(bf16x8, u32x4{pk_bf16(L::nibble_f32<0>(lo), L::nibble_f32<2>(lo)),
                                             pk_bf16(L::nibble_f32<0>(hi), L::nibble_f32<2>(hi)),
                                             pk_bf16(L::nibble_f32<1>(lo), L::nibble_f32<3>(lo)),
                                             pk_bf16(L::nibble_f32<1>(hi), L::nibble_f32<3>(hi))});
 }
+
+constexpr uint32_t KEY_SIGNS = 0x88888888u;   // keys' c + 8 to two's complement
 
 // max / sum over the four lanes that share lane % 16
 __device__ inline float quad_max(float x) {
@@ -96,7 +98,7 @@ struct RegTile {
     const CodeBits &bits;
     __device__ inline bf16x8 key(int sub, int m, int) const {
         const int w = sub * (D / 32) + m;
-        return EXACT ? exact_codes(t.k[w >> 2][w & 3]) : biased_codes(t.k[w >> 2][w & 3], bits);
+        return EXACT ? exact_codes(t.k[w >> 2][w & 3] ^ KEY_SIGNS) : biased_codes(t.k[w >> 2][w & 3], bits);
     }
     __device__ inline bf16x8 value(int c, int) const { return exact_codes(t.v[c >> 2][c & 3]); }
 };
@@ -534,7 +536,8 @@ __global__ void __launch_bounds__(256, WAVES) kv4_block_kernel(Kv4AttnArgs a, in
             const int x = wave + 4 * j;
             bf16x8 *to = ops[buf][x / (D / 32)] + x % (D / 32) * 256 + lane;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) to[e * 64] = exact_codes(word[j][e]);
+            for (int e = 0; e < 4; ++e)
+                to[e * 64] = exact_codes(x % (D / 32) < D / 64 ? word[j][e] ^ KEY_SIGNS : word[j][e]);
         }
         if (st < 2) scales[buf][st][sx] = scale;
         live[0] = next[0], live[1] = next[1];

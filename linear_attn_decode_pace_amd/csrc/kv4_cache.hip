@@ -123,8 +123,7 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(Kv4View c, const int32_
                 uint32_t word = 0u - BASE * 0x11111111u;   // takes BASE from every place
 #pragma unroll
                 for (int e = 0; e < 8; ++e) word += y[e] << (4 * ((e & 1) * 4 + (e >> 1)));
-                int nibble;
-                *(uint32_t *)(to + kv4_key_word(D, t, ch, &nibble)) = word;
+                *(uint32_t *)(to + kv4_key_word(D, t, ch)) = word;
             } else {   // the four channels of a packing thread side by side
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
@@ -148,7 +147,7 @@ __global__ void __launch_bounds__(256) kv4_append_kernel(Kv4View c, const int32_
     }
     if (!mask) return;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) word[i] |= old[i] & ~mask;
+    for (int i = 0; i < 4; ++i) word[i] = ((word[i] ^ 0x88888888u) & mask) | (old[i] & ~mask);   // c + 8 to two's complement
     *words = word;
 }
 
@@ -197,7 +196,7 @@ __global__ void __launch_bounds__(D) kv4_read_kernel(Kv4View c, const int32_t *s
             float *to = v + (size_t)(w.t0 + t) * row + base + 64 * group + n16;
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                to[16 * e] = live ? (float)((int)((words[e] >> (4 * i)) & 15) - 8) * s[i >> 2][i & 3] : 0.f;
+                to[16 * e] = live ? (float)(int)__builtin_amdgcn_sbfe(words[e], 4 * i, 4) * s[i >> 2][i & 3] : 0.f;
         }
     }
 }

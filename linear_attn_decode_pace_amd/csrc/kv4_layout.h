@@ -3,10 +3,11 @@
 // A page holds, for each key / value head, page_tokens / 32 tiles of 32
 // tokens.  A tile is contiguous: key codes (16 d bytes), value codes (16 d
 // bytes), key scales, value scales (each float32 [d / 64][32], one per group
-// of 64 channels and token).  Codes are stored as c + 8 (1..15), in the order
-// in which the attention kernel's matrix products take them, so that a lane's
-// operand is one 32-bit word of eight codes and a wavefront's load is 1 KiB
-// without gaps:
+// of 64 channels and token).  Codes are stored in the form that the attention
+// kernel unpacks cheapest, keys as c + 8 (1..15) and values in two's
+// complement, and in the order in which its matrix products take them, so that
+// a lane's operand is one 32-bit word of eight codes and a wavefront's load is
+// 1 KiB without gaps:
 //   key codes: word (sub, m) of lane 16 q + t, for token 16 sub + t of the
 //     tile, holds channels 32 m + 8 q + j, j = 0..7 (a k-slice of 32 channels
 //     of the product keys x queries; slices 2 g and 2 g + 1 are group g);
@@ -29,18 +30,10 @@ constexpr int KV4_GROUP = 64;  // channels that share a scale
 
 __host__ __device__ inline size_t kv4_tile_bytes(int d) { return (size_t)36 * d; }
 
-__device__ inline int kv4_word_offset(int w, int lane) { return ((w >> 2) * 64 + lane) * 16 + (w & 3) * 4; }
-
-// byte offset in a tile of the word with key (token t, channel c), and its nibble
-__device__ inline int kv4_key_word(int d, int t, int c, int *nibble) {
-    const int j = c & 7;
-    *nibble = (j & 1) * 4 + (j >> 1);
-    return kv4_word_offset((t >> 4) * (d >> 5) + (c >> 5), ((c >> 3) & 3) * 16 + (t & 15));
-}
-// byte offset of the value word, and its nibble
-__device__ inline int kv4_value_word(int d, int t, int c, int *nibble) {
-    *nibble = (t >> 4) * 4 + (t & 3);
-    return 16 * d + kv4_word_offset(c >> 4, ((t & 15) >> 2) * 16 + (c & 15));
+// byte offset in a tile of the word with channels c .. c + 7 of token t's key
+__device__ inline int kv4_key_word(int d, int t, int c) {
+    const int w = (t >> 4) * (d >> 5) + (c >> 5), lane = ((c >> 3) & 3) * 16 + (t & 15);
+    return ((w >> 2) * 64 + lane) * 16 + (w & 3) * 4;
 }
 __device__ inline int kv4_key_scales(int d) { return 32 * d; }
 __device__ inline int kv4_value_scales(int d) { return 34 * d; }
