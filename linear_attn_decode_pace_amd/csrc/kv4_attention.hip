@@ -80,11 +80,17 @@ struct TileRegs {
     typedef float scales_t __attribute__((ext_vector_type(D / 64)));
     u32x4 k[D / 64], v[D / 64];
     scales_t sc;
+    // ONCE: codes that no other workgroup of the call reads, past the caches
+    // (64 caches of up to 32768 tokens: 276 us against 288 us)
+    template <bool ONCE>
     __device__ inline void load(const uint8_t *tile, int lane) {
+        auto get = [](const uint8_t *p) {
+            return ONCE ? __builtin_nontemporal_load((const u32x4 *)p) : *(const u32x4 *)p;
+        };
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
-            k[i] = *(const u32x4 *)(tile + i * 1024 + lane * 16);
-            v[i] = *(const u32x4 *)(tile + 16 * D + i * 1024 + lane * 16);
+            k[i] = get(tile + i * 1024 + lane * 16);
+            v[i] = get(tile + 16 * D + i * 1024 + lane * 16);
         }
         sc = *(const scales_t *)(tile + 32 * D + lane * (D / 16));
     }
@@ -409,7 +415,7 @@ __global__ void __launch_bounds__(256, WAVES) kv4_attention_kernel(Kv4AttnArgs a
     auto fetch = [&](int j) {   // tile `ahead` into slot j
         const int tile = tile_of(ahead);
         live[j] = table.live(page);
-        buf[j].load(table.tile(page, tile), lane);
+        buf[j].template load<WR <= 2>(table.tile(page, tile), lane);   // WR <= 2: one row block
         ahead += A::WK;
         page = ahead < last ? table.page(tile_of(ahead)) : -1;
     };
