@@ -12,6 +12,15 @@
 // three float32 factors (M, the weighted scores, the weighted V) are taken in
 // three bf16 parts each, which keep their 24 bits, so outputs and state are as
 // exact as float32 products.
+//
+// 1024 states of 128 x 128 over 4096 tokens take 1.26 ms: 273 TFLOP/s of the
+// formulas above (without the parts' factor of three), 4.3 TB/s of q, k, v and o.
+// Neither matrix cores (38% busy) nor VALU (35%) nor LDS (23%) fill that time:
+// the shader clock falls to 1.9 GHz under it, and the phases of a chunk (scores,
+// Q M, update) depend on each other within two waves a SIMD.  With neither
+// loads nor stores it takes 1.02 ms, with a third of the products 1.16 ms.
+// 16 states over 16384 tokens are cut into 32 segments each: 44 us for the
+// segments' own states, 13 us to add them up, 88 us for the outputs.
 #include <algorithm>
 
 #include "mfma_common.h"

@@ -8,6 +8,10 @@
 // their heads and computes the tokens' sines and cosines once, into LDS: the
 // angle pos * freq needs float64 to be reduced (a float32 product of a far
 // position is off by whole radians), which is too slow to repeat for each head.
+//
+// 16384 rows of 32 + 8 heads of 128 channels, bf16, half of them rotated: 66 us,
+// 5.1 TB/s (a large copy reaches 6.6).  32 rows of 16 + 16 heads: 3.2 us, the
+// launch and one round of loads.
 #include <algorithm>
 
 #include "../../include/pace.h"
