@@ -429,9 +429,9 @@ int pace_qk_norm_rope(const pace_norm_config *cfg, const void *q, const void *k,
  * Linear attention with a fixed decay for each head:
  *     M_t = decay_h M_{t-1} + k_t v_t^T,   o_t = scale * M_t^T q_t,
  * over n_tok tokens of every (sequence, head), from a float32 state.  One
- * entry point for prompts and decode steps: bf16 calls of more than 16 tokens
- * run a chunked matrix-core kernel (split over the tokens where there are
- * few states), shorter ones and float32 inputs the recurrent form.
+ * entry point for prompts and decode steps: calls of more than 16 tokens run a
+ * chunked matrix-core kernel (split over the tokens where there are few
+ * states), shorter ones the recurrent form.
  *   d_k: 64 or 128; d_v: a multiple of 16, 16..256.
  *   q, k: device [n_tok, B, H, d_k], v: device [n_tok, B, H, d_v], in_dtype,
  *         16-byte aligned.
@@ -445,8 +445,9 @@ int pace_qk_norm_rope(const pace_norm_config *cfg, const void *q, const void *k,
  *   out: device float32 [n_tok, B, H, d_v].  state_*, out: 16-byte aligned.
  *   workspace: device, 16-byte aligned, at least pace_linear_attn_workspace()
  *         bytes; may be NULL where that is 0.  Its contents do not matter.
- * All sums and the state are float32.  The chunked kernel splits float32
- * factors into three bf16 parts (24 significant bits) for the matrix cores.
+ * All sums and the state are float32.  For bf16 inputs the chunked kernel
+ * splits float32 factors into three bf16 parts (24 significant bits) for the
+ * matrix cores; float32 inputs are multiplied as float32.
  * q, k and v of a sequence's tokens, and the state, must be finite: the
  * chunked form sums over whole chunks of 64 tokens, so a value that is not
  * reaches earlier tokens of its chunk too.

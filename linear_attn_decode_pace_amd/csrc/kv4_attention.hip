@@ -637,7 +637,7 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(Kv4AttnArgs a, int splits
 struct Plan {
     int nt, wr, row_blocks, splits;
 };
-Plan plan_for(const Kv4View &c, int G, int T, int window, int bf16) {
+Plan plan_for(const Kv4View &c, int G, int T, int bf16) {
     Plan p;
     const long long R = (long long)T * G;
     const bool wide = bf16 && c.d <= 128;   // registers for two row tiles a wave
@@ -648,11 +648,10 @@ Plan plan_for(const Kv4View &c, int G, int T, int window, int bf16) {
     const long long groups = (long long)c.B * c.Hk * p.row_blocks;
     // few rows: enough workgroups to fill the card a few times over (lengths
     // differ), but at least four tiles for each wave.  Many rows: their partial
-    // results cost more than idle units, so only until every unit has work.
+    // results cost more than idle units, so only to two workgroups a unit.
     const long long fill = p.wr == 4 ? 512 : 4096;
     const long long want = (fill + groups - 1) / groups, most = tiles / (4 * (4 / p.wr));
     p.splits = (int)std::max(1ll, std::min(std::min(want, most), 256ll));
-    (void)window;
     return p;
 }
 
@@ -662,8 +661,8 @@ void launch(const Kv4AttnArgs &a, const Plan &p, hipStream_t s) {
     if constexpr (NT == 2 && WR == 4) {
         hipLaunchKernelGGL((kv4_block_kernel<D, 2, 2>), grid, dim3(256), 0, s, a, p.row_blocks, p.splits);
     } else {
-    constexpr int PF = 2, WAVES = D <= 128 && QP == 1 ? (NT == 1 ? 2 : 1) : 1;
-    hipLaunchKernelGGL((kv4_attention_kernel<D, QP, NT, WR, PF, WAVES>), grid, dim3(256), 0, s, a, p.row_blocks, p.splits);
+        constexpr int PF = 2, WAVES = D <= 128 && QP == 1 && NT == 1 ? 2 : 1;
+        hipLaunchKernelGGL((kv4_attention_kernel<D, QP, NT, WR, PF, WAVES>), grid, dim3(256), 0, s, a, p.row_blocks, p.splits);
     }
     const long long rows = (long long)a.c.B * a.c.Hk * a.T * a.G;
     if (p.splits > 8 || (p.splits > 1 && rows <= 8192))
@@ -686,12 +685,12 @@ void dispatch(const Kv4AttnArgs &a, const Plan &p, hipStream_t s) {
 }  // namespace
 
 uint64_t kv4_attention_workspace(const Kv4View &c, int G, int T, int bf16) {
-    const Plan p = plan_for(c, G, T, 0, bf16);
+    const Plan p = plan_for(c, G, T, bf16);
     return p.splits == 1 ? 0 : (uint64_t)p.splits * c.B * c.Hk * T * G * (c.d + 4) * 4;
 }
 
 hipError_t launch_kv4_attention(const Kv4AttnArgs &a, int bf16, hipStream_t s) {
-    const Plan p = plan_for(a.c, a.G, a.T, a.window, bf16);
+    const Plan p = plan_for(a.c, a.G, a.T, bf16);
     if (a.c.d == 64)
         bf16 ? dispatch<64, 1>(a, p, s) : dispatch<64, 3>(a, p, s);
     else if (a.c.d == 128)

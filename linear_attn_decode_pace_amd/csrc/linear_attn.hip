@@ -1,8 +1,8 @@
 // Linear attention with a fixed decay g for each head:
 //     M_t = g M_{t-1} + k_t v_t^T,   o_t = scale M_t^T q_t.
 //
-// Recurrent form (decode steps, float32 inputs): the state goes through
-// registers, one read and one write of it bound the step.
+// Recurrent form (decode steps): the state goes through registers, one read and
+// one write of it bound the step.
 //
 // Chunked form (bf16 prompts): for the tokens i = 0..C-1 of a chunk and the
 // state M before it,
@@ -459,6 +459,195 @@ __global__ void __launch_bounds__(256, 2) linear_chunk_kernel(LinearArgs a, int 
     }
 }
 
+// float32 inputs: the same chunk algebra on float32 matrix products (16 x 16 x 4),
+// 32 tokens at a time.  Their k-slot is the lane group: with group x as row 4 x + r of a
+// 16-row tile, register r of an accumulator tile is an operand as it stands.
+// Bound by the matrix rate of float32 (a sixteenth of bf16): 128 states of 128 x 128
+// over 2048 tokens take 323 us (65 TFLOP/s), token by token 2630 us.  Calls of 17 to 33
+// tokens and 1024 states lose up to a tenth (46.6 us, 41.8 us), with fewer states they
+// gain (13.0 us, 19.5 us), so the switch stands at 16 tokens as for bf16.
+template <int DK, int CT, int MODE>
+__global__ void __launch_bounds__(256, 2) linear_chunk_f32_kernel(LinearArgs a, int col_blocks, int segs, int seg_len) {
+    constexpr int C = 32, RT = DK / 16, CB = 64 * CT;
+    constexpr int KP = C * (DK / 4) / 256, VP = C * (CB / 4) / 256;   // 16-byte pieces a thread moves
+    constexpr int ROW = DK + 4, VROW = CB + 4;
+    __shared__ __align__(16) float kx[C][ROW], qx[MODE == LIN_LOCAL ? 1 : C][ROW], vx[C][VROW];
+    __shared__ f32x4 px[3][MODE == LIN_LOCAL ? 1 : 64];               // weighted scores (0, 0), (1, 0), (1, 1)
+    __shared__ __align__(16) float rw[C], ps[C + 16];
+    const float *const K = (const float *)a.k, *const Q = (const float *)a.q, *const V = (const float *)a.v;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n16 = lane & 15, quad = lane >> 4;
+    const int BH = a.B * a.H;
+    const int bh = blockIdx.x % BH, rest = blockIdx.x / BH, cb = rest % col_blocks, seg = rest / col_blocks;
+    const int b = bh / a.H, h = bh - b * a.H;
+    const int len = a.lens ? min(max(a.lens[b], 0), a.T) : a.T;
+    const int lo = seg * seg_len, hi = min(len, lo + seg_len);
+    if (MODE != LIN_WHOLE && lo >= hi) return;
+    const int col0 = cb * CB + wave * 16 * CT;
+    const float g = a.decay[h];
+    for (int i = threadIdx.x; i < C + 16; i += 256) {
+        const float p = power(g, i - 15 < 0 ? 0 : i - 15);
+        ps[i] = i < 15 ? 0.f : a.scale * p;
+        if (i >= 15 && i < 15 + C) rw[C - 1 - (i - 15)] = p;
+    }
+    f32x4 M[RT][CT];
+    const size_t in_state = (size_t)bh * DK * a.dv + (size_t)(4 * quad) * a.dv + col0 + n16;
+    const float *from = MODE == LIN_WHOLE ? a.state_in : a.workspace + (size_t)seg * BH * DK * a.dv;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+        for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                M[rt][ct][r] = MODE != LIN_LOCAL && from && col0 + 16 * ct < a.dv
+                                   ? from[in_state + (size_t)(16 * rt + r) * a.dv + 16 * ct]
+                                   : 0.f;
+
+    // tokens fill the last rows of a chunk, as above
+    f32x4 kr[KP], qr[MODE == LIN_LOCAL ? 1 : KP], vr[VP];
+    const size_t kstep = (size_t)BH * DK, vstep = (size_t)BH * a.dv;
+    auto fetch = [&](int r0) {
+#pragma unroll
+        for (int i = 0; i < KP; ++i) {
+            const int u = threadIdx.x + 256 * i, row = u / (DK / 4), at = u % (DK / 4) * 4;
+            const size_t from = (size_t)max(r0 + row, lo) * kstep + (size_t)bh * DK + at;
+            kr[i] = *(const f32x4 *)(K + from);
+            if constexpr (MODE != LIN_LOCAL) qr[i] = *(const f32x4 *)(Q + from);
+        }
+#pragma unroll
+        for (int i = 0; i < VP; ++i) {
+            const int u = threadIdx.x + 256 * i, row = u / (CB / 4), at = cb * CB + u % (CB / 4) * 4;
+            vr[i] = *(const f32x4 *)(V + (size_t)max(r0 + row, lo) * vstep + (size_t)bh * a.dv + min(at, a.dv - 4));
+        }
+    };
+    auto put = [&](int skip) {
+        const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < KP; ++i) {
+            const int u = threadIdx.x + 256 * i, row = u / (DK / 4), at = u % (DK / 4) * 4;
+            *(f32x4 *)&kx[row][at] = row < skip ? zero : kr[i];
+            if constexpr (MODE != LIN_LOCAL) *(f32x4 *)&qx[row][at] = row < skip ? zero : qr[i];
+        }
+#pragma unroll
+        for (int i = 0; i < VP; ++i) {
+            const int u = threadIdx.x + 256 * i, row = u / (CB / 4);
+            *(f32x4 *)&vx[row][u % (CB / 4) * 4] = row < skip ? zero : vr[i];
+        }
+    };
+    if (lo < hi) {
+        const int skip = max(C - (hi - lo), 0);
+        fetch(lo - skip);
+        put(skip);
+    }
+    local_barrier();
+    for (int c0 = lo; c0 < hi; c0 += C) {
+        const int cl = min(C, hi - c0), skip = C - cl, r0 = c0 - skip;
+        const bool more = c0 + C < hi;
+        const int skip2 = max(C - (hi - c0 - C), 0);
+        if (more) fetch(c0 + C - skip2);
+        f32x4 o[2][CT];
+        if constexpr (MODE != LIN_LOCAL) {
+            if (wave < 3) {   // tile (i, j) of the weighted scores, transposed
+                const int i = wave > 0, j = wave > 1;
+                f32x4 s = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    const f32x4 kf = *(const f32x4 *)&kx[16 * j + n16][16 * rt + 4 * quad];
+                    const f32x4 qf = *(const f32x4 *)&qx[16 * i + n16][16 * rt + 4 * quad];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) s = mfma_f32_k4(kf[r], qf[r], s);
+                }
+                const float *w = ps + 15 + 16 * (i - j) + n16 - 4 * quad;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) s[r] *= w[-r];
+                px[wave][lane] = s;
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) o[i][ct] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) {
+                f32x4 qf[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) qf[i] = *(const f32x4 *)&qx[16 * i + n16][16 * rt + 4 * quad];
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) o[i][ct] = mfma_f32_k4(M[rt][ct][r], qf[i][r], o[i][ct]);
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const float w = ps[max(16 + 16 * i + n16 - skip, 0)];
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) o[i][ct] *= w;
+            }
+            local_barrier();   // the scores of all waves are there
+        }
+        const float gc = cl == C ? rw[0] * g : rw[C - 1 - cl];
+        if (more || MODE != LIN_OUTPUTS) {
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) M[rt][ct] *= gc;
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            f32x4 p[2];   // of query tiles 0 and 1; keys 16..31 reach only the second
+            if constexpr (MODE != LIN_LOCAL) p[0] = px[0][lane], p[1] = px[1 + j][lane];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const int t = 16 * j + 4 * quad + r;
+                float v[CT];
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct) v[ct] = vx[t][wave * 16 * CT + 16 * ct + n16];
+                if constexpr (MODE != LIN_LOCAL) {
+#pragma unroll
+                    for (int i = j; i < 2; ++i)
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) o[i][ct] = mfma_f32_k4(v[ct], p[i][r], o[i][ct]);
+                }
+                if (more || MODE != LIN_OUTPUTS) {
+                    const float w = rw[t];
+#pragma unroll
+                    for (int rt = 0; rt < RT; ++rt) {
+                        const float kk = kx[t][16 * rt + n16];
+#pragma unroll
+                        for (int ct = 0; ct < CT; ++ct) M[rt][ct] = mfma_f32_k4(kk, v[ct] * w, M[rt][ct]);
+                    }
+                }
+            }
+        }
+        if constexpr (MODE != LIN_LOCAL) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (16 * i + n16 < skip) continue;
+#pragma unroll
+                for (int ct = 0; ct < CT; ++ct)
+                    if (col0 + 16 * ct < a.dv)
+                        *(f32x4 *)(a.out + (size_t)(r0 + 16 * i + n16) * vstep + (size_t)bh * a.dv + col0 + 16 * ct + 4 * quad) = o[i][ct];
+            }
+        }
+        if (more) {
+            local_barrier();
+            put(skip2);
+            local_barrier();
+        }
+    }
+    if constexpr (MODE != LIN_OUTPUTS) {
+        float *to = MODE == LIN_WHOLE ? a.state_out : a.workspace + (size_t)seg * BH * DK * a.dv;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int ct = 0; ct < CT; ++ct)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    if (col0 + 16 * ct < a.dv) to[in_state + (size_t)(16 * rt + r) * a.dv + 16 * ct] = M[rt][ct][r];
+    }
+}
+
 // The states before each segment from those that the segments leave alone,
 // in place in the workspace, and the state behind the last token
 __global__ void __launch_bounds__(256) linear_prefix_kernel(LinearArgs a, int segs, int seg_len, int blocks) {
@@ -494,17 +683,17 @@ struct LinearPlan {
     bool chunked;
     int ct, col_blocks, segs, seg_len;
 };
-LinearPlan linear_plan(int B, int H, int dk, int dv, int T, int bf16) {
-    // (the chunked kernel's offsets within a chunk have 32 bits)
-    LinearPlan p{bf16 && T > 16 && (double)B * H * std::max(dk, dv) * 64 < 4294967296.0, dv <= 64 ? 1 : 2, 1, 1, T};
+LinearPlan linear_plan(int B, int H, int dk, int dv, int T) {
+    // (the bf16 kernel's offsets within a chunk have 32 bits)
+    LinearPlan p{T > 16 && (double)B * H * std::max(dk, dv) * 64 < 4294967296.0, dv <= 64 ? 1 : 2, 1, 1, T};
     if (!p.chunked) return p;
     p.col_blocks = (dv + 64 * p.ct - 1) / (64 * p.ct);
     const long long groups = (long long)B * H * p.col_blocks, chunks = (T + LC - 1) / LC;
     // a segment reads K and V twice and moves 8 d_k d_v bytes of states: at least
     // four chunks of it, and only until two workgroups a unit are there, or three
     // where the states are half as large (16 states of 16384 tokens, d_k = 128:
-    // 146 us with 512 workgroups, 172 us with 768 and 165 us with 256; 84 states of up to
-    // 1999 tokens, d_k = 64: 64 us with 512, 55 us with 768)
+    // 146 us with 512 workgroups, 172 us with 768 and 165 us with 256 when chosen; 84
+    // states of up to 1999 tokens, d_k = 64: 64 us with 512, 55 us with 768)
     const long long want = groups >= 256 ? 1 : (dk == 64 ? 768 : 512) / groups;
     const long long segs = std::max(1ll, std::min(want, chunks / 4));
     p.seg_len = (int)((chunks + segs - 1) / segs) * LC;
@@ -512,34 +701,39 @@ LinearPlan linear_plan(int B, int H, int dk, int dv, int T, int bf16) {
     return p;
 }
 
+template <int DK, int CT, int MODE>
+void launch_chunk(const LinearArgs &a, const LinearPlan &p, int bf16, hipStream_t s) {
+    const dim3 grid((unsigned)((long long)a.B * a.H * p.col_blocks * p.segs));
+    auto go = [&](auto kernel) {
+        hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a, p.col_blocks, p.segs, p.seg_len);
+    };
+    bf16 ? go(linear_chunk_kernel<DK, CT, MODE>) : go(linear_chunk_f32_kernel<DK, CT, MODE>);
+}
+
 template <int DK, int CT>
-void launch_chunks(const LinearArgs &a, const LinearPlan &p, hipStream_t s) {
-    const dim3 grid((unsigned)((long long)a.B * a.H * p.col_blocks * p.segs)), wg(256);
-    if (p.segs == 1) {
-        hipLaunchKernelGGL((linear_chunk_kernel<DK, CT, LIN_WHOLE>), grid, wg, 0, s, a, p.col_blocks, 1, p.seg_len);
-        return;
-    }
+void launch_chunks(const LinearArgs &a, const LinearPlan &p, int bf16, hipStream_t s) {
+    if (p.segs == 1) return launch_chunk<DK, CT, LIN_WHOLE>(a, p, bf16, s);
     const int blocks = (a.dk * a.dv / 4 + 255) / 256;
-    hipLaunchKernelGGL((linear_chunk_kernel<DK, CT, LIN_LOCAL>), grid, wg, 0, s, a, p.col_blocks, p.segs, p.seg_len);
-    hipLaunchKernelGGL(linear_prefix_kernel, dim3((unsigned)((long long)a.B * a.H * blocks)), wg, 0, s, a, p.segs,
+    launch_chunk<DK, CT, LIN_LOCAL>(a, p, bf16, s);
+    hipLaunchKernelGGL(linear_prefix_kernel, dim3((unsigned)((long long)a.B * a.H * blocks)), dim3(256), 0, s, a, p.segs,
                        p.seg_len, blocks);
-    hipLaunchKernelGGL((linear_chunk_kernel<DK, CT, LIN_OUTPUTS>), grid, wg, 0, s, a, p.col_blocks, p.segs, p.seg_len);
+    launch_chunk<DK, CT, LIN_OUTPUTS>(a, p, bf16, s);
 }
 
 }  // namespace
 
-uint64_t linear_attn_workspace(int B, int H, int dk, int dv, int T, int bf16) {
-    const LinearPlan p = linear_plan(B, H, dk, dv, T, bf16);
+uint64_t linear_attn_workspace(int B, int H, int dk, int dv, int T) {
+    const LinearPlan p = linear_plan(B, H, dk, dv, T);
     return p.segs == 1 ? 0 : (uint64_t)p.segs * B * H * dk * dv * 4;
 }
 
 hipError_t launch_linear_attn(const LinearArgs &a, int bf16, hipStream_t s) {
-    const LinearPlan p = linear_plan(a.B, a.H, a.dk, a.dv, a.T, bf16);
+    const LinearPlan p = linear_plan(a.B, a.H, a.dk, a.dv, a.T);
     if (p.chunked) {
         if (a.dk == 128)
-            p.ct == 1 ? launch_chunks<128, 1>(a, p, s) : launch_chunks<128, 2>(a, p, s);
+            p.ct == 1 ? launch_chunks<128, 1>(a, p, bf16, s) : launch_chunks<128, 2>(a, p, bf16, s);
         else
-            p.ct == 1 ? launch_chunks<64, 1>(a, p, s) : launch_chunks<64, 2>(a, p, s);
+            p.ct == 1 ? launch_chunks<64, 1>(a, p, bf16, s) : launch_chunks<64, 2>(a, p, bf16, s);
         return hipGetLastError();
     }
     if (bf16) return a.dk == 128 ? launch_step<uint16_t, 128>(a, s) : launch_step<uint16_t, 64>(a, s);

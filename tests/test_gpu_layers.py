@@ -176,6 +176,30 @@ def test_linear_attention(t, b, h, dk, dv, dtype, ragged, start):
         assert s2 is s and torch.equal(bits(s), bits(state_got)) and torch.equal(bits(again), bits(got))
 
 
+@pytest.mark.parametrize("t,b,h,dk,dv,ragged,start", [
+    (17, 3, 3, 128, 128, True, True),                  # shorter than one chunk of 32
+    (32, 2, 2, 64, 64, False, True),
+    (33, 2, 3, 128, 240, True, True),
+    (64, 2, 2, 64, 16, False, False),
+    (95, 3, 3, 128, 64, True, True),
+    (700, 1, 3, 128, 128, False, True),                # segments
+    (1030, 3, 1, 64, 208, True, True),
+    (2048, 1, 1, 128, 256, False, False),
+])
+def test_linear_attention_float32_prompts(t, b, h, dk, dv, ragged, start):
+    test_linear_attention(t, b, h, dk, dv, F32, ragged, start)
+    q, k, v, decay, state, lens = linear_inputs(t, t, b, h, dk, dv, F32, True, start)
+    dev = [x.cuda() for x in (q, k, v, decay)]
+    state = None if state is None else state.cuda()
+    one = rt().linear_attention(*dev, state=state, lens=lens.cuda(), out=torch.zeros(v.shape, device="cuda"))
+    for i in range(b):                                 # what stands behind the end is not read
+        for x in dev[:3]:
+            x[min(int(lens[i]), t):, i] = math.nan
+    two = rt().linear_attention(*dev, state=state, lens=lens.cuda(), out=torch.zeros(v.shape, device="cuda"))
+    for x, y in zip(one, two):
+        assert torch.equal(bits(x), bits(y))
+
+
 def test_linear_attention_prompt_then_steps():
     """A prompt in two calls, then single tokens, equals one call over all of them."""
     t, b, h, d = 150, 2, 3, 128
