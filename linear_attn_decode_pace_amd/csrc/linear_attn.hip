@@ -463,9 +463,9 @@ __global__ void __launch_bounds__(256, 2) linear_chunk_kernel(LinearArgs a, int 
 // 32 tokens at a time.  Their k-slot is the lane group: with group x as row 4 x + r of a
 // 16-row tile, register r of an accumulator tile is an operand as it stands.
 // Bound by the matrix rate of float32 (a sixteenth of bf16): 128 states of 128 x 128
-// over 2048 tokens take 323 us (65 TFLOP/s), token by token 2630 us.  Calls of 17 to 33
+// over 2048 tokens take 293 us (72 TFLOP/s), token by token 2630 us.  Calls of 17 to 33
 // tokens and 1024 states lose up to a tenth (46.6 us, 41.8 us), with fewer states they
-// gain (13.0 us, 19.5 us), so the switch stands at 16 tokens as for bf16.
+// gain (11.6 us, 19.5 us), so the switch stands at 16 tokens as for bf16.
 template <int DK, int CT, int MODE>
 __global__ void __launch_bounds__(256, 2) linear_chunk_f32_kernel(LinearArgs a, int col_blocks, int segs, int seg_len) {
     constexpr int C = 32, RT = DK / 16, CB = 64 * CT;
@@ -683,10 +683,14 @@ struct LinearPlan {
     bool chunked;
     int ct, col_blocks, segs, seg_len;
 };
-LinearPlan linear_plan(int B, int H, int dk, int dv, int T) {
+LinearPlan linear_plan(int B, int H, int dk, int dv, int T, int bf16) {
     // (the bf16 kernel's offsets within a chunk have 32 bits)
     LinearPlan p{T > 16 && (double)B * H * std::max(dk, dv) * 64 < 4294967296.0, dv <= 64 ? 1 : 2, 1, 1, T};
     if (!p.chunked) return p;
+    // float32: half the columns a workgroup where units would idle, as its chunks are
+    // bound by a wave's products (128 states of 128 x 128: 256 tokens 40 us against 57,
+    // 2048 tokens 293 against 323; 1024 states 252 against 220, so not there)
+    if (!bf16 && (long long)B * H * ((dv + 127) / 128) < 256) p.ct = 1;
     p.col_blocks = (dv + 64 * p.ct - 1) / (64 * p.ct);
     const long long groups = (long long)B * H * p.col_blocks, chunks = (T + LC - 1) / LC;
     // a segment reads K and V twice and moves 8 d_k d_v bytes of states: at least
@@ -722,13 +726,13 @@ void launch_chunks(const LinearArgs &a, const LinearPlan &p, int bf16, hipStream
 
 }  // namespace
 
-uint64_t linear_attn_workspace(int B, int H, int dk, int dv, int T) {
-    const LinearPlan p = linear_plan(B, H, dk, dv, T);
+uint64_t linear_attn_workspace(int B, int H, int dk, int dv, int T, int bf16) {
+    const LinearPlan p = linear_plan(B, H, dk, dv, T, bf16);
     return p.segs == 1 ? 0 : (uint64_t)p.segs * B * H * dk * dv * 4;
 }
 
 hipError_t launch_linear_attn(const LinearArgs &a, int bf16, hipStream_t s) {
-    const LinearPlan p = linear_plan(a.B, a.H, a.dk, a.dv, a.T);
+    const LinearPlan p = linear_plan(a.B, a.H, a.dk, a.dv, a.T, bf16);
     if (p.chunked) {
         if (a.dk == 128)
             p.ct == 1 ? launch_chunks<128, 1>(a, p, bf16, s) : launch_chunks<128, 2>(a, p, bf16, s);

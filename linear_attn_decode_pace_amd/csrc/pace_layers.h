@@ -38,7 +38,7 @@ struct LinearArgs {
     float scale;
     int B, H, dk, dv, T;
 };
-uint64_t linear_attn_workspace(int B, int H, int dk, int dv, int T);
+uint64_t linear_attn_workspace(int B, int H, int dk, int dv, int T, int bf16);
 hipError_t launch_linear_attn(const LinearArgs &a, int bf16, hipStream_t s);
 
 // ---- 4-bit paged cache (kv4_cache.hip, kv4_attention.hip) ------------------

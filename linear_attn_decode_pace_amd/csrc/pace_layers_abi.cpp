@@ -123,7 +123,7 @@ PACE_API int pace_linear_attn_workspace(int32_t batch, int32_t heads, int32_t d_
     if (!out) return fail(PACE_EINVAL, "out must not be NULL");
     int rc = check_linear(batch, heads, d_k, d_v, n_tok, in_dtype);
     if (rc) return rc;
-    *out = linear_attn_workspace(batch, heads, d_k, d_v, n_tok);
+    *out = linear_attn_workspace(batch, heads, d_k, d_v, n_tok, in_dtype == PACE_DTYPE_BF16);
     return ok();
 }
 
@@ -142,7 +142,7 @@ PACE_API int pace_linear_attn(int32_t batch, int32_t heads, int32_t d_k, int32_t
     if ((rc = check_i32(lens, "lens", false))) return rc;
     if (!isfinite(scale)) return fail(PACE_EINVAL, "scale must be finite");
     const int bf16 = in_dtype == PACE_DTYPE_BF16;
-    const uint64_t need = linear_attn_workspace(batch, heads, d_k, d_v, n_tok);
+    const uint64_t need = linear_attn_workspace(batch, heads, d_k, d_v, n_tok, bf16);
     if (need && (!workspace || !aligned(workspace, 16) || workspace_bytes < need))
         return fail(PACE_EINVAL, "workspace must be 16-byte aligned and hold %llu bytes", (unsigned long long)need);
     LinearArgs a{q,   k,         v,   decay,                        lens,  state_in, state_out,

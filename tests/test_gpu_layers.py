@@ -185,6 +185,8 @@ def test_linear_attention(t, b, h, dk, dv, dtype, ragged, start):
     (700, 1, 3, 128, 128, False, True),                # segments
     (1030, 3, 1, 64, 208, True, True),
     (2048, 1, 1, 128, 256, False, False),
+    (70, 64, 5, 128, 128, True, True),                 # wide column blocks
+    (37, 43, 6, 64, 240, True, False),
 ])
 def test_linear_attention_float32_prompts(t, b, h, dk, dv, ragged, start):
     test_linear_attention(t, b, h, dk, dv, F32, ragged, start)
