@@ -80,33 +80,35 @@ __device__ inline float quad_sum(float x) {
     return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
-// a wavefront's share of one tile: its operand words, and D / 64 of the tile's
-// 2 D scales, which the wave spreads through LDS when it comes to the tile
-template <int D>
+// a wavefront's share of one tile: the operand words of D of its CH D channels,
+// and D / 64 of their 2 D scales, which the wave spreads through LDS when it comes
+// to the tile
+template <int D, int CH>
 struct TileRegs {
+    static_assert(CH == 1 || D == 128, "a half has whole groups of four words");
     typedef float scales_t __attribute__((ext_vector_type(D / 64)));
     u32x4 k[D / 64], v[D / 64];
     scales_t sc;
     // ONCE: codes that no other workgroup of the call reads, past the caches
     // (64 caches of up to 32768 tokens: 276 us against 288 us)
     template <bool ONCE>
-    __device__ inline void load(const uint8_t *tile, int lane) {
+    __device__ inline void load(const uint8_t *tile, int half, int lane) {
         auto get = [](const uint8_t *p) {
             return ONCE ? __builtin_nontemporal_load((const u32x4 *)p) : *(const u32x4 *)p;
         };
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
-            k[i] = get(tile + i * 1024 + lane * 16);
-            v[i] = get(tile + 16 * D + i * 1024 + lane * 16);
+            k[i] = get(tile + (i * CH + half) * 1024 + lane * 16);
+            v[i] = get(tile + 16 * CH * D + (half * (D / 64) + i) * 1024 + lane * 16);
         }
-        sc = *(const scales_t *)(tile + 32 * D + lane * (D / 16));
+        sc = *(const scales_t *)(tile + 32 * CH * D + half * 2 * D + lane * (D / 16) + (lane >> 5) * 2 * (CH - 1) * D);
     }
 };
 
 // operands of a tile from its words in registers, with D floats of LDS for its scales
-template <int D, bool EXACT>
+template <int D, int CH, bool EXACT>
 struct RegTile {
-    const TileRegs<D> &t;
+    const TileRegs<D, CH> &t;
     const float *scales;
     const CodeBits &bits;
     __device__ inline bf16x8 key(int sub, int m, int) const {
@@ -125,13 +127,12 @@ struct SharedTile {
     __device__ inline bf16x8 value(int c, int lane) const { return ops[(D / 16 + c) * 64 + lane]; }
 };
 
-// What a workgroup works on: 16 NT rows for each of WR row waves, and 4 / WR
-// waves that share a row wave's tiles.
-template <int D, int QP, int NT, int WR, bool EXACT>
+// What a wave works on: 16 NT rows, D channels (from ch0 on) of a head
+template <int D, int QP, int NT, bool EXACT>
 struct Attn {
-    static constexpr int NG = D / 64, NM = D / 32, NC = D / 16, WK = 4 / WR;
+    static constexpr int NG = D / 64, NM = D / 32, NC = D / 16;
     bf16x8 q[NT][QP][NM];
-    f32x4 qoff[NT][NG];
+    float qoff[NT][NG];
     f32x4 o[NT][NC];
     float m[NT], l[NT];
     int at[NT];   // last position that the lane's row sees, -1 for none
@@ -139,7 +140,7 @@ struct Attn {
     int window, sinks;
 
     // queries of rows r0 .. as operands, empty sums
-    __device__ inline void init(const Kv4AttnArgs &a, int b, int h, int r0, int len, int n, int lane) {
+    __device__ inline void init(const Kv4AttnArgs &a, int b, int h, int ch0, int r0, int len, int n, int lane) {
         const int n16 = lane & 15, quad = lane >> 4, R = a.T * a.G;
         window = a.window, sinks = a.sinks;
         const float sign = a.scale < 0.f ? -1.f : 1.f;
@@ -149,7 +150,7 @@ struct Attn {
             const int r = r0 + nt * 16 + n16, t = r / a.G;
             const bool ok = r < R && t < n;
             at[nt] = ok ? len - n + t : -1;
-            const size_t row = (((size_t)t * a.c.B + b) * a.c.Hk * a.G + (size_t)h * a.G + (r - t * a.G)) * D;
+            const size_t row = (((size_t)t * a.c.B + b) * a.c.Hk * a.G + (size_t)h * a.G + (r - t * a.G)) * a.c.d + ch0;
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
                 float sum = 0.f;
@@ -182,8 +183,7 @@ struct Attn {
                         q[nt][part][i] = __builtin_bit_cast(bf16x8, v);
                     }
                 }
-                const float off = -CODE_BIAS * quad_sum(sum);
-                qoff[nt][g] = f32x4{off, off, off, off};
+                qoff[nt][g] = -CODE_BIAS * quad_sum(sum);
             }
 #pragma unroll
             for (int i = 0; i < NC; ++i) o[nt][i] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -204,24 +204,31 @@ struct Attn {
     // one tile, positions p0 .. p0 + 31; full: every row sees all of them
     template <class Tile>
     __device__ inline void step(const Tile &t, int p0, bool full, int lane) {
-        const float *lds = t.scales;   // key scales [group][token], then value scales
         f32x4 sc[NT][2];
+        scores(t, sc, lane);
+        gather(t, sc, p0, full, lane);
+    }
+
+    // what the wave's channels give to the scores
+    template <class Tile>
+    __device__ inline void scores(const Tile &t, f32x4 (&sc)[NT][2], int lane) {
+        const float *lds = t.scales;   // key scales [group][token], then value scales
 #pragma unroll
         for (int s = 0; s < 2; ++s) {
-            bf16x8 ka[NM];
-#pragma unroll
-            for (int i = 0; i < NM; ++i)
-                ka[i] = t.key(s, i, lane);
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
+                // (operands of few products at a time: registers)
+                if (D == 256) __builtin_amdgcn_sched_barrier(0);
+                const bf16x8 ka[2] = {t.key(s, 2 * g, lane), t.key(s, 2 * g + 1, lane)};
                 const f32x4 ks = *(const f32x4 *)(lds + g * 32 + s * 16 + (lane >> 4) * 4);   // tokens 4 quad ..
 #pragma unroll
                 for (int nt = 0; nt < NT; ++nt) {
-                    f32x4 acc = EXACT ? f32x4{0.f, 0.f, 0.f, 0.f} : qoff[nt][g];
+                    const float off = EXACT ? 0.f : qoff[nt][g];
+                    f32x4 acc = {off, off, off, off};
 #pragma unroll
                     for (int i = 2 * g; i < 2 * g + 2; ++i)
 #pragma unroll
-                        for (int part = QP - 1; part >= 0; --part) acc = mfma_bf16_k32(ka[i], q[nt][part][i], acc);
+                        for (int part = QP - 1; part >= 0; --part) acc = mfma_bf16_k32(ka[i - 2 * g], q[nt][part][i], acc);
                     if (g == 0) {
                         sc[nt][s] = acc * ks;
                     } else {
@@ -232,6 +239,12 @@ struct Attn {
             }
             __builtin_amdgcn_sched_barrier(0);
         }
+    }
+
+    // softmax and values
+    template <class Tile>
+    __device__ inline void gather(const Tile &t, f32x4 (&sc)[NT][2], int p0, bool full, int lane) {
+        const float *lds = t.scales;
         f32x4 vs[NG][2];
 #pragma unroll
         for (int g = 0; g < NG; ++g)
@@ -299,6 +312,7 @@ struct Attn {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < NC; ++i) {
+            if (D == 256 && i && i % 4 == 0) __builtin_amdgcn_sched_barrier(0);
             const bf16x8 va = t.value(i, lane);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
@@ -358,10 +372,10 @@ __device__ inline void store4(void *out, size_t i, f32x4 x) {
         *(f32x4 *)((float *)out + i) = x;
 }
 
-// a wave's rows: the result, or its part of it
+// a wave's rows and channels: the result, or its part of it
 template <int D, int QP, int NT, class A>
-__device__ inline void store_rows(const Kv4AttnArgs &a, const A &w, int b, int h, int r0, int n, int split, int splits,
-                                  int lane) {
+__device__ inline void store_rows(const Kv4AttnArgs &a, const A &w, int b, int h, int ch0, int r0, int n, int split,
+                                  int splits, int lane) {
     const int n16 = lane & 15, quad = lane >> 4, R = a.T * a.G, bh = b * a.c.Hk + h;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
@@ -369,28 +383,42 @@ __device__ inline void store_rows(const Kv4AttnArgs &a, const A &w, int b, int h
         if (r >= R || t >= n) continue;
         if (splits == 1) {
             const float inv = w.l[nt] > 0.f ? 1.f / w.l[nt] : 0.f;
-            const size_t at = (((size_t)t * a.c.B * a.c.Hk + bh) * a.G + (r - t * a.G)) * D;
+            const size_t at = (((size_t)t * a.c.B * a.c.Hk + bh) * a.G + (r - t * a.G)) * D + ch0;
 #pragma unroll
             for (int x = 0; x < A::NC; ++x) store4<QP>(a.out, at + 16 * x + 4 * quad, w.o[nt][x] * inv);
         } else {
             float *p = partial_row(a, D, split, bh, r);
 #pragma unroll
-            for (int x = 0; x < A::NC; ++x) *(f32x4 *)(p + 16 * x + 4 * quad) = w.o[nt][x];
-            if (quad == 0) *(f32x2 *)(p + D) = f32x2{w.m[nt], w.l[nt]};
+            for (int x = 0; x < A::NC; ++x) *(f32x4 *)(p + ch0 + 16 * x + 4 * quad) = w.o[nt][x];
+            if (quad == 0 && ch0 == 0) *(f32x2 *)(p + D) = f32x2{w.m[nt], w.l[nt]};
         }
     }
 }
 
-template <int D, int QP, int NT, int WR, int PF, int WAVES>
+// Workgroup barrier that orders LDS only: loads of the tiles ahead stay in flight
+__device__ inline void local_barrier() {
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// Few rows.  The four waves of a workgroup are WR row waves of 16 NT rows, CH parts
+// of the channels and WK waves that take tiles in turn.  CH = 2 for heads of 256
+// channels: the registers of a whole head leave one wave a SIMD; halves of a head,
+// which add their scores through LDS, leave two (64 caches of up to 4096 tokens, 8 such
+// heads, four query heads each: 115 us against 190 us, float32 in proportion).
+template <int D, int QP, int NT, int WR, int CH, int PF, int WAVES>
 __global__ void __launch_bounds__(256, WAVES) kv4_attention_kernel(Kv4AttnArgs a, int row_blocks, int splits) {
     constexpr bool EXACT = QP == 3;
-    using A = Attn<D, QP, NT, WR, EXACT>;
+    constexpr int DW = D / CH, WK = 4 / (WR * CH);
+    using A = Attn<DW, QP, NT, EXACT>;
     constexpr int ROWS = 16 * NT * WR, LDW = D + 4;
-    __shared__ float scales[4][D];
+    __shared__ float scales[4][DW];
+    __shared__ f32x4 parts[CH == 1 ? 1 : 2][4][NT * 2][64];   // of the scores, for two tiles in turn
     const Kv4View &c = a.c;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n16 = lane & 15, quad = lane >> 4;
-    const int wr = wave / A::WK, wk = wave % A::WK;
+    const int wr = wave / (4 / WR), wk = wave / CH % WK, half = wave % CH;
     const int BH = c.B * c.Hk, R = a.T * a.G;
     // (sequence, head) runs fastest: the row blocks that share a head's cache
     // then meet in one XCD's L2 where B * Hk is a multiple of 8; the last rows,
@@ -405,8 +433,9 @@ __global__ void __launch_bounds__(256, WAVES) kv4_attention_kernel(Kv4AttnArgs a
 
     const CodeBits bits;
 
-    const TileList list(a, r0, 16 * NT, len, n);
-    const int at_lo = list.at_lo, at_hi = list.at_hi;
+    // (waves that meet at barriers walk the same tiles)
+    const TileList mine(a, r0, 16 * NT, len, n), list = CH == 1 ? mine : TileList(a, rb * ROWS, ROWS, len, n);
+    const int at_lo = mine.at_lo, at_hi = mine.at_hi;
     const int per = (list.total + splits - 1) / splits;
     const int first = min(split * per, list.total), last = min(first + per, list.total);
     auto tile_of = [&](int i) { return list.tile(i); };
@@ -415,35 +444,55 @@ __global__ void __launch_bounds__(256, WAVES) kv4_attention_kernel(Kv4AttnArgs a
     // PF - 1 are under way and the table entry of the one behind them is read
     // (past the last tile, and where a tile has no page, the pool's first tile
     // is loaded and not used: loads without branches can be waited for one by one)
-    TileRegs<D> buf[PF];
+    TileRegs<DW, CH> buf[PF];
     bool live[PF];
     int i = first + wk, ahead = i;
     int page = ahead < last ? table.page(tile_of(ahead)) : -1;
     auto fetch = [&](int j) {   // tile `ahead` into slot j
         const int tile = tile_of(ahead);
         live[j] = table.live(page);
-        buf[j].template load<WR <= 2>(table.tile(page, tile), lane);   // WR <= 2: one row block
-        ahead += A::WK;
+        buf[j].template load<true>(table.tile(page, tile), half, lane);
+        ahead += WK;
         page = ahead < last ? table.page(tile_of(ahead)) : -1;
     };
 #pragma unroll
     for (int j = 0; j < PF - 1; ++j) fetch(j);
     A w;   // the queries' loads follow those of the first tiles
-    w.init(a, b, h, r0, len, n, lane);
-    while (i < last) {
+    w.init(a, b, h, half * DW, r0, len, n, lane);
+    const int stop = CH == 1 ? last : last + wk;   // CH = 2: as many steps for each wave
+    while (i < stop) {
 #pragma unroll
         for (int j = 0; j < PF; ++j) {
-            if (i >= last) break;
+            if (i >= stop) break;
             fetch((j + PF - 1) % PF);
-            const int p0 = tile_of(i) * KV4_TILE;
-            i += A::WK;
-            if (!live[j]) continue;
+            const int tile = tile_of(i), p0 = tile * KV4_TILE;
+            bool use = live[j];
+            if (CH > 1) use = use && i < last && p0 <= at_hi && (tile < mine.n_sink || tile >= mine.lo);
+            i += WK;
+            if (CH == 1 && !use) continue;
             const bool full = p0 + KV4_TILE - 1 <= at_lo &&
                               (a.window == 0 || p0 > at_hi - a.window || p0 + KV4_TILE <= a.sinks);
-            *(typename TileRegs<D>::scales_t *)(scales[wave] + lane * A::NG) = buf[j].sc;
-            wave_sync();
-            const RegTile<D, EXACT> t{buf[j], scales[wave], bits};
-            if (full)
+            const RegTile<DW, CH, EXACT> t{buf[j], scales[wave], bits};
+            if (use) {
+                *(typename TileRegs<DW, CH>::scales_t *)(scales[wave] + lane * A::NG) = buf[j].sc;
+                wave_sync();
+            }
+            if constexpr (CH == 2) {
+                f32x4 sc[NT][2];
+                if (use) {
+                    w.scores(t, sc, lane);
+#pragma unroll
+                    for (int x = 0; x < NT * 2; ++x) parts[j][wave][x][lane] = sc[x / 2][x % 2];
+                }
+                local_barrier();
+                if (!use) continue;
+#pragma unroll
+                for (int x = 0; x < NT * 2; ++x) sc[x / 2][x % 2] += parts[j][wave ^ 1][x][lane];
+                if (full)
+                    w.gather(t, sc, p0, true, lane);
+                else
+                    w.gather(t, sc, p0, false, lane);
+            } else if (full)
                 w.step(t, p0, true, lane);
             else
                 w.step(t, p0, false, lane);
@@ -452,17 +501,17 @@ __global__ void __launch_bounds__(256, WAVES) kv4_attention_kernel(Kv4AttnArgs a
 
     w.close();
     const size_t out_row = ((size_t)b * c.Hk + h) * a.G;   // + t * B * Hk * G + head
-    if constexpr (A::WK == 1) {
-        store_rows<D, QP, NT>(a, w, b, h, r0, n, split, splits, lane);
+    if constexpr (WK == 1) {
+        store_rows<D, QP, NT>(a, w, b, h, half * DW, r0, n, split, splits, lane);
     } else {
-        __shared__ float part[4][16][LDW];
+        __shared__ float part[4 / CH][16][LDW];
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
             if (nt) __syncthreads();
-            float *mine = part[wave][n16];
+            float *own = part[wave / CH][n16];
 #pragma unroll
-            for (int x = 0; x < A::NC; ++x) *(f32x4 *)(mine + 16 * x + 4 * quad) = w.o[nt][x];
-            if (quad == 0) mine[D] = w.m[nt], mine[D + 1] = w.l[nt];
+            for (int x = 0; x < A::NC; ++x) *(f32x4 *)(own + half * DW + 16 * x + 4 * quad) = w.o[nt][x];
+            if (quad == 0 && half == 0) own[D] = w.m[nt], own[D + 1] = w.l[nt];
             __syncthreads();
             for (int u = threadIdx.x; u < WR * 16 * (D / 4); u += 256) {
                 const int x = u % (D / 4), row = u / (D / 4), g = row / 16, rr = row % 16;
@@ -470,12 +519,12 @@ __global__ void __launch_bounds__(256, WAVES) kv4_attention_kernel(Kv4AttnArgs a
                 if (r >= R || t >= n) continue;
                 float top = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < A::WK; ++k) top = fmaxf(top, part[g * A::WK + k][rr][D]);
+                for (int k = 0; k < WK; ++k) top = fmaxf(top, part[g * WK + k][rr][D]);
                 f32x4 sum = {0.f, 0.f, 0.f, 0.f};
                 float l = 0.f;
 #pragma unroll
-                for (int k = 0; k < A::WK; ++k) {
-                    const float *p = part[g * A::WK + k][rr];
+                for (int k = 0; k < WK; ++k) {
+                    const float *p = part[g * WK + k][rr];
                     const float f = p[D] > -INFINITY ? __builtin_amdgcn_exp2f(p[D] - top) : 0.f;
                     sum += f * *(const f32x4 *)(p + 4 * x);
                     l = fmaf(f, p[D + 1], l);
@@ -493,27 +542,22 @@ __global__ void __launch_bounds__(256, WAVES) kv4_attention_kernel(Kv4AttnArgs a
     }
 }
 
-// Workgroup barrier that orders LDS only: loads of the tiles ahead stay in flight
-__device__ inline void local_barrier() {
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
-}
-
-// Many rows (blocks of a prompt): four waves of 32 rows unpack each pair of
-// tiles once, into LDS in operand order, and all read it; the next pair's
-// loads and unpacking run beside this one's products.  512 tokens of two sequences,
-// 32 heads, behind a window of 4096: 140 + 11 us, 458 TFLOP/s, bound by the
-// VALU work of the softmax (about 100 instructions for 16 rows and 32 tokens, against
-// 16 matrix products) at two waves a SIMD; one row tile a wave and three or
-// four waves took 180 us and more.
-template <int D, int NT, int WAVES>
-__global__ void __launch_bounds__(256, WAVES) kv4_block_kernel(Kv4AttnArgs a, int row_blocks, int splits) {
+// Many rows (blocks of a prompt): four waves of 16 NT rows unpack each TP tiles
+// once, into LDS in operand order, and all read them; the loads and the unpacking of the
+// next run beside these ones' products.  TP = 2 but for heads of 256 channels,
+// where LDS has room for one tile twice.  512 tokens of two sequences, 32 heads of 128,
+// behind a window of 4096: 140 + 11 us, 458 TFLOP/s, bound by the VALU work of the
+// softmax (about 100 instructions for 16 rows and 32 tokens, against 16 matrix
+// products) at two waves a SIMD; one row tile a wave and three or four waves took 180 us
+// and more.  512 tokens of 16 sequences of 4096, 32 heads of 256: 2.11 ms, 488 TFLOP/s
+// (3.47 ms with tiles unpacked by each wave), bound by reading operands from LDS.
+template <int D, int QP, int NT, int TP>
+__global__ void __launch_bounds__(256, 2) kv4_block_kernel(Kv4AttnArgs a, int row_blocks, int splits) {
     constexpr int ROWS = 64 * NT, NW = D / 8;   // operands of a tile
-    constexpr int NL = D / 64;                      // 16-byte loads of a lane for a pair: D / 16 KiB in all
-    using A = Attn<D, 1, NT, 4, true>;
-    __shared__ bf16x8 ops[2][2][NW * 64];
-    __shared__ float scales[2][2][D];
+    constexpr int NL = TP * D / 128;                // 16-byte loads of a lane for TP tiles: TP D / 32 KiB in all
+    using A = Attn<D, QP, NT, true>;
+    __shared__ bf16x8 ops[2][TP][NW * 64];
+    __shared__ float scales[2][TP][D];
     const Kv4View &c = a.c;
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int BH = c.B * c.Hk, R = a.T * a.G;
@@ -525,17 +569,17 @@ __global__ void __launch_bounds__(256, WAVES) kv4_block_kernel(Kv4AttnArgs a, in
     if (rb * ROWS / a.G >= n) return;
     const int r0 = rb * ROWS + wave * 16 * NT;
     A w;
-    w.init(a, b, h, r0, len, n, lane);
+    w.init(a, b, h, 0, r0, len, n, lane);
 
     const TileList list(a, rb * ROWS, ROWS, len, n), mine(a, r0, 16 * NT, len, n);
-    const int per = ((list.total + splits - 1) / splits + 1) & ~1;
+    const int per = ((list.total + splits - 1) / splits + TP - 1) / TP * TP;
     const int first = min(split * per, list.total), last = min(first + per, list.total);
     const TileTable<D> table(c, b, h);
     u32x4 word[NL];
     float scale = 0.f;
-    const int st = threadIdx.x / D, sx = threadIdx.x % D;   // a thread's scale: tile of the pair, place
-    int live[2] = {}, next[2] = {};   // whether the pair's tiles have a page
-    auto fetch = [&](int i) {   // tiles i and i + 1 of the list
+    const int st = threadIdx.x / D, sx = threadIdx.x % D;   // a thread's scale: tile of the TP, place
+    int live[2] = {}, next[2] = {};   // whether the tiles have a page
+    auto fetch = [&](int i) {   // tiles i (and i + 1) of the list
         const int t0 = list.tile(i), t1 = list.tile(min(i + 1, last - 1));
         const int g0 = table.page(t0), g1 = table.page(t1);
         const uint8_t *p0 = table.tile(g0, t0), *p1 = table.tile(g1, t1);
@@ -545,7 +589,7 @@ __global__ void __launch_bounds__(256, WAVES) kv4_block_kernel(Kv4AttnArgs a, in
             const int x = wave + 4 * j;
             word[j] = *(const u32x4 *)((x < D / 32 ? p0 : p1) + x % (D / 32) * 1024 + lane * 16);
         }
-        if (st < 2) scale = ((const float *)((st ? p1 : p0) + 32 * D))[sx];
+        if (st < TP) scale = ((const float *)((st ? p1 : p0) + 32 * D))[sx];
     };
     auto unpack = [&](int buf) {
 #pragma unroll
@@ -556,7 +600,7 @@ __global__ void __launch_bounds__(256, WAVES) kv4_block_kernel(Kv4AttnArgs a, in
             for (int e = 0; e < 4; ++e)
                 to[e * 64] = exact_codes(x % (D / 32) < D / 64 ? word[j][e] ^ KEY_SIGNS : word[j][e]);
         }
-        if (st < 2) scales[buf][st][sx] = scale;
+        if (st < TP) scales[buf][st][sx] = scale;
         live[0] = next[0], live[1] = next[1];
     };
     if (first < last) {
@@ -565,11 +609,11 @@ __global__ void __launch_bounds__(256, WAVES) kv4_block_kernel(Kv4AttnArgs a, in
     }
     local_barrier();
     int buf = 0;
-    for (int i = first; i < last; i += 2, buf ^= 1) {
-        const bool more = i + 2 < last;
-        if (more) fetch(i + 2);
+    for (int i = first; i < last; i += TP, buf ^= 1) {
+        const bool more = i + TP < last;
+        if (more) fetch(i + TP);
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int j = 0; j < TP; ++j) {
             const int tile = list.tile(i + j), p0 = tile * KV4_TILE;
             // none, without a page, or not one of this wave's rows
             if (!live[j] || p0 > mine.at_hi || (tile >= mine.n_sink && tile < mine.lo)) continue;
@@ -585,7 +629,7 @@ __global__ void __launch_bounds__(256, WAVES) kv4_block_kernel(Kv4AttnArgs a, in
         local_barrier();
     }
     w.close();
-    store_rows<D, 1, NT>(a, w, b, h, r0, n, split, splits, lane);
+    store_rows<D, QP, NT>(a, w, b, h, 0, r0, n, split, splits, lane);
 }
 
 // Joins the splits of a row.  W waves take its splits in turn; W = 1: one wave a
@@ -658,12 +702,11 @@ Plan plan_for(const Kv4View &c, int G, int T, int bf16) {
 template <int D, int QP, int NT, int WR>
 void launch(const Kv4AttnArgs &a, const Plan &p, hipStream_t s) {
     const dim3 grid((unsigned)((long long)a.c.B * a.c.Hk * p.row_blocks * p.splits));
-    if constexpr (NT == 2 && WR == 4) {
-        hipLaunchKernelGGL((kv4_block_kernel<D, 2, 2>), grid, dim3(256), 0, s, a, p.row_blocks, p.splits);
-    } else {
-        constexpr int PF = 2, WAVES = D <= 128 && QP == 1 && NT == 1 ? 2 : 1;
-        hipLaunchKernelGGL((kv4_attention_kernel<D, QP, NT, WR, PF, WAVES>), grid, dim3(256), 0, s, a, p.row_blocks, p.splits);
-    }
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a, p.row_blocks, p.splits); };
+    if constexpr (WR == 4)
+        go(kv4_block_kernel<D, QP, NT, D == 256 ? 1 : 2>);
+    else
+        go(kv4_attention_kernel<D, QP, NT, WR, D == 256 ? 2 : 1, 2, NT == 1 ? 2 : 1>);
     const long long rows = (long long)a.c.B * a.c.Hk * a.T * a.G;
     if (p.splits > 8 || (p.splits > 1 && rows <= 8192))
         hipLaunchKernelGGL((kv4_join_kernel<D, QP, 4>), dim3((unsigned)rows), dim3(256), 0, s, a, p.splits);
@@ -673,11 +716,11 @@ void launch(const Kv4AttnArgs &a, const Plan &p, hipStream_t s) {
 
 template <int D, int QP>
 void dispatch(const Kv4AttnArgs &a, const Plan &p, hipStream_t s) {
+    if (p.wr == 1) return launch<D, QP, 1, 1>(a, p, s);
     if constexpr (QP == 1 && D <= 128) {
         if (p.nt == 2) return p.wr == 2 ? launch<D, QP, 2, 2>(a, p, s) : launch<D, QP, 2, 4>(a, p, s);
-        return p.wr == 1 ? launch<D, QP, 1, 1>(a, p, s) : launch<D, QP, 1, 2>(a, p, s);
+        return launch<D, QP, 1, 2>(a, p, s);
     } else {
-        if (p.wr == 1) return launch<D, QP, 1, 1>(a, p, s);
         return p.wr == 2 ? launch<D, QP, 1, 2>(a, p, s) : launch<D, QP, 1, 4>(a, p, s);
     }
 }

@@ -392,6 +392,23 @@ def test_cache_attention(b, hk, group, t, n, d, page, window, sinks, holes, dtyp
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("b,hk,group,t,n,d,page,window,sinks,holes", [
+    (3, 2, 5, 4, 300, 256, 64, 0, 0, True),            # two row tiles of wide heads
+    (2, 1, 8, 4, 500, 256, 32, 45, 10, True),
+    (2, 2, 3, 11, 420, 256, 128, 30, 0, False),        # more
+    (2, 1, 4, 90, 700, 256, 32, 100, 40, True),
+    (1, 1, 2, 1, 3000, 256, 32, 0, 0, False),          # split over the cache
+    (1, 1, 3, 25, 1200, 256, 32, 0, 0, True),
+    (2, 1, 1, 2, 2500, 128, 32, 100, 5, False),        # windows far shorter than the cache
+    (1, 2, 4, 100, 1500, 128, 64, 200, 0, False),
+    (1, 1, 8, 1, 2600, 64, 32, 64, 64, True),
+    (2, 1, 5, 9, 2100, 256, 96, 333, 1, False),
+])
+def test_cache_attention_wide_heads_and_long_caches(b, hk, group, t, n, d, page, window, sinks, holes, dtype):
+    test_cache_attention(b, hk, group, t, n, d, page, window, sinks, holes, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 def test_cache_attention_of_large_scores(dtype):
     """Scores far apart (a softmax of one), and all equal."""
     b, hk, d, page, n = 1, 1, 64, 32, 100
