@@ -681,21 +681,43 @@ __global__ void __launch_bounds__(256) kv4_join_kernel(Kv4AttnArgs a, int splits
 struct Plan {
     int nt, wr, row_blocks, splits;
 };
-Plan plan_for(const Kv4View &c, int G, int T, int bf16) {
+// at most what a row block sees of a cache with a window: see TileList
+long long window_tiles(int window, int sinks, int rows, int G) {
+    return ((long long)window + (rows + G - 1) / G) / KV4_TILE + 2 + ((long long)sinks + KV4_TILE - 1) / KV4_TILE;
+}
+Plan plan_for(const Kv4View &c, int G, int T, int window, int sinks, int bf16) {
     Plan p;
-    const long long R = (long long)T * G;
-    const bool wide = bf16 && c.d <= 128;   // registers for two row tiles a wave
-    p.nt = wide && R > 32 ? 2 : 1;
-    p.wr = R <= 16 ? 1 : (R <= 32 || (wide && R <= 64)) ? 2 : 4;
-    p.row_blocks = (int)((R + 16 * p.nt * p.wr - 1) / (16 * p.nt * p.wr));
-    const long long tiles = ((long long)c.max_pages * c.page_tokens + KV4_TILE - 1) / KV4_TILE;
-    const long long groups = (long long)c.B * c.Hk * p.row_blocks;
-    // few rows: enough workgroups to fill the card a few times over (lengths
-    // differ), but at least four tiles for each wave.  Many rows: their partial
-    // results cost more than idle units, so only to two workgroups a unit.
-    const long long fill = p.wr == 4 ? 512 : 4096;
-    const long long want = (fill + groups - 1) / groups, most = tiles / (4 * (4 / p.wr));
-    p.splits = (int)std::max(1ll, std::min(std::min(want, most), 256ll));
+    const long long R = (long long)T * G, heads = (long long)c.B * c.Hk;
+    auto tiles_of = [&](int rows) {   // at most what a row block sees
+        const long long all = ((long long)c.max_pages * c.page_tokens + KV4_TILE - 1) / KV4_TILE;
+        const long long seen = ((long long)window + rows / G + 1) / KV4_TILE + 2 + ((long long)sinks + KV4_TILE - 1) / KV4_TILE;
+        return window ? std::min(all, seen) : all;
+    };
+    // 16 or 32 rows a wave (registers: 32 for bf16 heads of up to 128 channels).  32
+    // halve the unpacking for a row and double a workgroup's, so they pay where a
+    // workgroup, two to a unit, has 24 tiles or more: 64 tokens of 32 heads in a cache of 8192,
+    // 8 tiles, 37 us with 16 rows and 45 with 32; 256 tokens, 32 tiles, 98 and 91 us.  At 33
+    // to 64 rows, halves of a tile list (WR = 2) with 32 rows a wave beat four waves
+    // of 16 for 64 channels (37 and 39 us for 160 heads), not for 128 (34 and 25 us for 55).
+    const bool wide = bf16 && c.d <= 128;
+    p.nt = wide && (R <= 64 ? R > 32 && c.d == 64 : heads * ((R + 127) / 128) * tiles_of(128) >= 24 * 512) ? 2 : 1;
+    p.wr = R <= 16 ? 1 : R <= (p.nt == 2 ? 64 : 32) ? 2 : 4;
+    const int rows = 16 * p.nt * p.wr;
+    p.row_blocks = (int)((R + rows - 1) / rows);
+    const long long groups = heads * p.row_blocks, tiles = tiles_of(rows);
+    if (p.wr == 4) {
+        // many rows: their partial results cost more than idle units, so only to
+        // two workgroups a unit
+        p.splits = (int)std::min(512 / groups, tiles / 4);
+    } else {
+        // few rows: to two workgroups a unit at four tiles a wave, and beyond, as lengths
+        // differ, to sixteen at 32 tiles (at four: 64 caches of up to 1024 tokens, 23 us against
+        // 16; of 4096 tokens, 256 channels, 117 against 105)
+        const int wk = std::max(1, 4 / (p.wr * (c.d == 256 ? 2 : 1)));   // waves that share a row's tiles
+        p.splits = (int)std::max(std::min((511 + groups) / groups, tiles / (4 * wk)),
+                                 std::min((4095 + groups) / groups, tiles / (32 * wk)));
+    }
+    p.splits = std::max(1, std::min(p.splits, 256));
     return p;
 }
 
@@ -718,8 +740,10 @@ template <int D, int QP>
 void dispatch(const Kv4AttnArgs &a, const Plan &p, hipStream_t s) {
     if (p.wr == 1) return launch<D, QP, 1, 1>(a, p, s);
     if constexpr (QP == 1 && D <= 128) {
-        if (p.nt == 2) return p.wr == 2 ? launch<D, QP, 2, 2>(a, p, s) : launch<D, QP, 2, 4>(a, p, s);
-        return launch<D, QP, 1, 2>(a, p, s);
+        if constexpr (D == 64)
+            if (p.nt == 2 && p.wr == 2) return launch<D, QP, 2, 2>(a, p, s);
+        if (p.nt == 2) return launch<D, QP, 2, 4>(a, p, s);
+        return p.wr == 2 ? launch<D, QP, 1, 2>(a, p, s) : launch<D, QP, 1, 4>(a, p, s);
     } else {
         return p.wr == 2 ? launch<D, QP, 1, 2>(a, p, s) : launch<D, QP, 1, 4>(a, p, s);
     }
@@ -728,12 +752,12 @@ void dispatch(const Kv4AttnArgs &a, const Plan &p, hipStream_t s) {
 }  // namespace
 
 uint64_t kv4_attention_workspace(const Kv4View &c, int G, int T, int bf16) {
-    const Plan p = plan_for(c, G, T, bf16);
+    const Plan p = plan_for(c, G, T, 0, 0, bf16);
     return p.splits == 1 ? 0 : (uint64_t)p.splits * c.B * c.Hk * T * G * (c.d + 4) * 4;
 }
 
 hipError_t launch_kv4_attention(const Kv4AttnArgs &a, int bf16, hipStream_t s) {
-    const Plan p = plan_for(a.c, a.G, a.T, bf16);
+    const Plan p = plan_for(a.c, a.G, a.T, a.window, a.sinks, bf16);
     if (a.c.d == 64)
         bf16 ? dispatch<64, 1>(a, p, s) : dispatch<64, 3>(a, p, s);
     else if (a.c.d == 128)
