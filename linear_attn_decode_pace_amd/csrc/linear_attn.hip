@@ -22,6 +22,7 @@
 // 16 states over 16384 tokens are cut into 32 segments each: 44 us for the
 // segments' own states, 13 us to add them up, 88 us for the outputs.
 #include <algorithm>
+#include <type_traits>
 
 #include "mfma_common.h"
 #include "pace_layers.h"
@@ -29,85 +30,195 @@
 namespace pace {
 namespace {
 
+// four elements as floats
+template <class T>
+__device__ inline f32x4 in_four(const void *p, size_t i) {
+    if constexpr (sizeof(T) == 2) {
+        const u32x2 w = *(const u32x2 *)((const uint16_t *)p + i);
+        return f32x4{lo_f32(w[0]), hi_f32(w[0]), lo_f32(w[1]), hi_f32(w[1])};
+    }
+    return *(const f32x4 *)((const float *)p + i);
+}
+
 template <class T>
 __device__ inline float in_elem(const void *p, size_t i) {
     if constexpr (sizeof(T) == 2) return bf2f(((const uint16_t *)p)[i]);
     return ((const float *)p)[i];
 }
 
-// Recurrent form.  One workgroup per (sequence, head, block of 4 CG columns):
-// a thread holds 4 adjacent columns of DK / RG state rows in registers over
-// all tokens, so the state is read and written once.  o_t = M_t^T q_t is
-// summed over a thread's rows, then over the row groups in LDS.
+// Recurrent form.  One workgroup per (sequence, head, block of 4 CG columns): a
+// thread holds 4 adjacent columns of DK / RG state rows in registers over all
+// tokens, so the state is read and written once.
 // STREAM: states larger than the last-level cache are read and written past
-// it (16384 states of 128 x 128: 368 us, 5.9 TB/s, against 393 us).
-template <class T, int DK, int CG, bool STREAM>
-__global__ void __launch_bounds__(256) linear_step_kernel(LinearArgs a, int col_blocks) {
-    constexpr int RG = 256 / CG, NR = DK / RG;
-    __shared__ f32x4 part[RG][CG];
-    __shared__ float kq[2][DK];
-    const int cb = blockIdx.x % col_blocks, bh = blockIdx.x / col_blocks;
-    const int b = bh / a.H, h = bh - b * a.H;
-    const int cg = threadIdx.x % CG, rg = threadIdx.x / CG, col = (cb * CG + cg) * 4;
-    const int n = a.lens ? min(max(a.lens[b], 0), a.T) : a.T;
-    const float g = a.decay[h];
-    const size_t base = (size_t)bh * DK * a.dv + (size_t)(rg * NR) * a.dv + col;
+// it (16384 states of 128 x 128: 361 us, 6.0 TB/s, 25 us less).
+// ONE: one column block; otherwise a state's blocks follow each other on one XCD, as
+// they share lines of it (15756 states of 128 x 48: 147 us, blocks in the order
+// of the grid 198 us).
+template <int DK, int CG, bool STREAM, bool ONE>
+struct StepState {
+    static constexpr int RG = 256 / CG, NR = DK / RG;
+    int bh, col0, cg, rg, n;
+    float g;
     f32x4 M[NR];
-#pragma unroll
-    for (int i = 0; i < NR; ++i) {
-        const f32x4 *from = (const f32x4 *)(a.state_in + base + (size_t)i * a.dv);
-        M[i] = !a.state_in ? f32x4{0.f, 0.f, 0.f, 0.f} : STREAM ? __builtin_nontemporal_load(from) : *from;
+    __device__ inline bool place(const LinearArgs &a, int col_blocks) {
+        int cb = 0;
+        bh = blockIdx.x;
+        if constexpr (!ONE) {
+            const int turn = blockIdx.x / 8;
+            cb = turn % col_blocks, bh = turn / col_blocks * 8 + blockIdx.x % 8;
+        }
+        cg = threadIdx.x % CG, rg = threadIdx.x / CG, col0 = cb * CG * 4;
+        return ONE || bh < a.B * a.H;
     }
-    for (int t = 0; t < n; ++t) {
-        const size_t row = (size_t)t * a.B * a.H + bh;
-        __syncthreads();
-        for (int i = threadIdx.x; i < 2 * DK; i += 256)
-            kq[i / DK][i % DK] = in_elem<T>(i < DK ? a.k : a.q, row * DK + i % DK);
-        f32x4 v;
+    __device__ inline size_t base(const LinearArgs &a) const {
+        return (size_t)bh * DK * a.dv + (size_t)(rg * NR) * a.dv + col0 + cg * 4;
+    }
+    __device__ inline void load(const LinearArgs &a) {
+        const int b = bh / a.H;
+        n = a.lens ? min(max(a.lens[b], 0), a.T) : a.T;
+        g = a.decay[bh - b * a.H];
+        const size_t at = base(a);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = in_elem<T>(a.v, row * a.dv + col + e);
-        __syncthreads();
+        for (int i = 0; i < NR; ++i) {
+            const f32x4 *from = (const f32x4 *)(a.state_in + at + (size_t)i * a.dv);
+            M[i] = !a.state_in ? f32x4{0.f, 0.f, 0.f, 0.f} : STREAM ? __builtin_nontemporal_load(from) : *from;
+        }
+    }
+    __device__ inline void store(const LinearArgs &a) const {
+        const size_t at = base(a);
+#pragma unroll
+        for (int i = 0; i < NR; ++i) {
+            f32x4 *to = (f32x4 *)(a.state_out + at + (size_t)i * a.dv);
+            if (STREAM)
+                __builtin_nontemporal_store(M[i], to);
+            else
+                *to = M[i];
+        }
+    }
+    // one token; returns what the thread's rows give to its output
+    __device__ inline f32x4 step(const float *k, const float *q, f32x4 v) {
         f32x4 o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < NR; ++i) {
-            const float kk = kq[0][rg * NR + i], qq = kq[1][rg * NR + i];
+            const float kk = k[rg * NR + i], qq = q[rg * NR + i];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 M[i][e] = fmaf(kk, v[e], M[i][e] * g);
                 o[e] = fmaf(qq, M[i][e], o[e]);
             }
         }
-        part[rg][cg] = o;
+        return o;
+    }
+};
+
+// A single token: its output is summed over the row groups in LDS (in a wave's lanes first,
+// as below, costs registers and with them a wave a SIMD: 378 us for those 16384 states)
+template <class T, int DK, int CG, bool STREAM, bool ONE>
+__global__ void __launch_bounds__(256) linear_token_kernel(LinearArgs a, int col_blocks) {
+    using S = StepState<DK, CG, STREAM, ONE>;
+    __shared__ f32x4 part[S::RG][CG];
+    __shared__ float kq[2][DK];
+    S s;
+    if (!s.place(a, col_blocks)) return;
+    s.load(a);
+    if (s.n > 0) {
+        for (int i = threadIdx.x; i < 2 * DK; i += 256)
+            kq[i / DK][i % DK] = in_elem<T>(i < DK ? a.k : a.q, (size_t)s.bh * DK + i % DK);
+        f32x4 v;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = in_elem<T>(a.v, (size_t)s.bh * a.dv + s.col0 + s.cg * 4 + e);
         __syncthreads();
-        if (rg == 0) {
+        part[s.rg][s.cg] = s.step(kq[0], kq[1], v);
+        __syncthreads();
+        if (s.rg == 0) {
             f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-            for (int r = 0; r < RG; ++r) sum += part[r][cg];
-            *(f32x4 *)(a.out + row * a.dv + col) = sum * a.scale;
+            for (int r = 0; r < S::RG; ++r) sum += part[r][s.cg];
+            *(f32x4 *)(a.out + (size_t)s.bh * a.dv + s.col0 + s.cg * 4) = sum * a.scale;
         }
     }
+    s.store(a);
+}
+
+// Several tokens: q, k and v of TB tokens are fetched at a time, into LDS, and o_t =
+// M_t^T q_t is summed over a thread's rows, a wave's lanes, and for the TB tokens
+// together the waves in LDS (15756 states of 128 x 48, 8 tokens: 203 us, with a
+// token's loads and sums after each other 436 us)
+template <class T, int DK, int CG, bool STREAM, bool ONE>
+__global__ void __launch_bounds__(256) linear_step_kernel(LinearArgs a, int col_blocks) {
+    constexpr int TB = 8;
+    using S = StepState<DK, CG, STREAM, ONE>;
+    __shared__ f32x4 part[TB][4][CG], vs[TB][CG];
+    __shared__ __align__(16) float kq[TB][2][DK];
+    S s;
+    if (!s.place(a, col_blocks)) return;
+    s.load(a);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, bh = s.bh, col0 = s.col0;
+    const size_t BH = (size_t)a.B * a.H;
+    for (int t0 = 0; t0 < s.n; t0 += TB) {
+        const int m = min(TB, s.n - t0);
+        if (t0) __syncthreads();
+        for (int u = threadIdx.x; u < m * (DK / 2); u += 256) {
+            const int t = u / (DK / 2), x = u % (DK / 2), what = x / (DK / 4), at = x % (DK / 4) * 4;
+            *(f32x4 *)&kq[t][what][at] = in_four<T>(what ? a.q : a.k, ((t0 + t) * BH + bh) * DK + at);
+        }
+        for (int u = threadIdx.x; u < m * CG; u += 256)
+            vs[u / CG][u % CG] = in_four<T>(a.v, ((t0 + u / CG) * BH + bh) * a.dv + col0 + u % CG * 4);
+        __syncthreads();
+        for (int t = 0; t < m; ++t) {
+            const f32x4 o = s.step(kq[t][0], kq[t][1], vs[t][s.cg]);
+            // over the wave's lanes of a column group, halving what a lane holds in each step
+            const bool hi = lane & CG, hi2 = lane & (2 * CG);
+            float x = hi ? o[2] : o[0], y = hi ? o[3] : o[1];
+            x += __shfl_xor(hi ? o[0] : o[2], CG);
+            y += __shfl_xor(hi ? o[1] : o[3], CG);
+            float *to = (float *)&part[t][wave][s.cg] + 2 * hi;
+            if constexpr (CG == 32) {
+                *(f32x2 *)to = f32x2{x, y};
+            } else {
+                float z = hi2 ? y : x;
+                z += __shfl_xor(hi2 ? x : y, 2 * CG);
 #pragma unroll
-    for (int i = 0; i < NR; ++i) {
-        f32x4 *to = (f32x4 *)(a.state_out + base + (size_t)i * a.dv);
-        if (STREAM)
-            __builtin_nontemporal_store(M[i], to);
-        else
-            *to = M[i];
+                for (int d = 4 * CG; d < 64; d <<= 1) z += __shfl_xor(z, d);
+                if (lane < 4 * CG) to[hi2] = z;
+            }
+        }
+        __syncthreads();
+        for (int u = threadIdx.x; u < m * CG; u += 256) {
+            const int t = u / CG, x = u % CG;
+            const f32x4 sum = (part[t][0][x] + part[t][1][x]) + (part[t][2][x] + part[t][3][x]);
+            *(f32x4 *)(a.out + ((t0 + t) * BH + bh) * a.dv + col0 + x * 4) = sum * a.scale;
+        }
     }
+    s.store(a);
+}
+
+template <class T, int DK, int CG>
+void launch_step_columns(const LinearArgs &a, hipStream_t s) {
+    const int cb = a.dv / (4 * CG);
+    const dim3 grid((unsigned)(cb == 1 ? (long long)a.B * a.H : ((long long)a.B * a.H + 7) / 8 * 8 * cb));
+    // (rows of 64 bytes share lines: 1313 x 12 states of 128 x 112, 331 us, 388 us past the cache)
+    const bool stream = (double)a.B * a.H * a.dk * a.dv * 4 > 256e6;
+    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, dim3(256), 0, s, a, cb); };
+    auto form = [&](auto past, auto one) {
+        constexpr bool STREAM = decltype(past)::value, ONE = decltype(one)::value;
+        a.T == 1 ? go(linear_token_kernel<T, DK, CG, STREAM, ONE>) : go(linear_step_kernel<T, DK, CG, STREAM, ONE>);
+    };
+    auto columns = [&](auto past) { cb == 1 ? form(past, std::true_type()) : form(past, std::false_type()); };
+    if constexpr (CG > 4)
+        if (stream) return columns(std::true_type());
+    columns(std::false_type());
 }
 
 template <class T, int DK>
 hipError_t launch_step(const LinearArgs &a, hipStream_t s) {
-    const int cg = a.dv % 128 == 0 ? 32 : a.dv % 64 == 0 ? 16 : a.dv % 32 == 0 ? 8 : 4;
-    const int cb = a.dv / (4 * cg);
-    const dim3 grid((unsigned)((long long)a.B * a.H * cb)), wg(256);
-    const bool stream = (double)a.B * a.H * a.dk * a.dv * 4 > 256e6;
-    auto go = [&](auto kernel) { hipLaunchKernelGGL(kernel, grid, wg, 0, s, a, cb); };
-    switch (cg) {
-        case 32: stream ? go(linear_step_kernel<T, DK, 32, true>) : go(linear_step_kernel<T, DK, 32, false>); break;
-        case 16: stream ? go(linear_step_kernel<T, DK, 16, true>) : go(linear_step_kernel<T, DK, 16, false>); break;
-        case 8: stream ? go(linear_step_kernel<T, DK, 8, true>) : go(linear_step_kernel<T, DK, 8, false>); break;
-        default: stream ? go(linear_step_kernel<T, DK, 4, true>) : go(linear_step_kernel<T, DK, 4, false>); break;
-    }
+    if (a.dv % 128 == 0)
+        launch_step_columns<T, DK, 32>(a, s);
+    else if (a.dv % 64 == 0)
+        launch_step_columns<T, DK, 16>(a, s);
+    else if (a.dv % 32 == 0)
+        launch_step_columns<T, DK, 8>(a, s);
+    else
+        launch_step_columns<T, DK, 4>(a, s);
     return hipGetLastError();
 }
 

@@ -202,6 +202,40 @@ def test_linear_attention_float32_prompts(t, b, h, dk, dv, ragged, start):
         assert torch.equal(bits(x), bits(y))
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("t,b,h,dk,dv,ragged,start", [
+    (1, 7, 3, 128, 48, True, True),                    # column blocks that share lines of the state
+    (1, 3, 3, 64, 112, False, False),
+    (2, 5, 1, 128, 80, True, True),
+    (7, 3, 5, 64, 192, True, True),
+    (8, 4, 2, 128, 32, False, True),
+    (9, 4, 3, 128, 16, True, True),
+    (15, 1, 1, 64, 96, False, False),
+    (16, 9, 3, 128, 128, True, True),
+])
+def test_linear_attention_steps_of_odd_widths(t, b, h, dk, dv, ragged, start, dtype):
+    """Per element.  A state element is a sum over tokens whose terms pass at
+    most t roundings of a product with g and t of a sum, so it is off by at most
+    2 t u of the same sum over absolute values; an output adds d_k products of
+    it, one rounding each, in some order, and the scale: (2 t + d_k + 8) u of the
+    same formula over absolute values, rigorous to first order in u.  (Relative to the
+    result itself no bound holds: one token's output is (q . k) v, and a
+    product q . k of unit vectors can cancel to anything.)"""
+    q, k, v, decay, state, lens = linear_inputs(t + dv, t, b, h, dk, dv, dtype, ragged, start)
+    want, end = ref.linear(q, k, v, decay, state, lens, dk ** -0.5)
+    size = lambda x: None if x is None else x.abs()  # noqa: E731
+    mass, end_mass = ref.linear(size(q), size(k), size(v), decay, size(state), lens, dk ** -0.5)
+    dev = lambda x: None if x is None else x.cuda()  # noqa: E731
+    out = torch.full((t, b, h, dv), 7.0, device="cuda")
+    args = [x.cuda() for x in (q, k, v, decay)]
+    got, state_got = rt().linear_attention(*args, state=dev(state), lens=dev(lens), scale=dk ** -0.5, out=out)
+    got, state_got = got.cpu().double(), state_got.cpu().double()
+    live = ~torch.isnan(want)
+    assert (got[~live] == 7.0).all()
+    assert ((got - want).abs()[live] <= ((2 * t + dk + 8) * ref.U32 * mass)[live]).all()
+    assert ((state_got - end).abs() <= 2 * t * ref.U32 * 1.001 * end_mass).all()
+
+
 def test_linear_attention_prompt_then_steps():
     """A prompt in two calls, then single tokens, equals one call over all of them."""
     t, b, h, d = 150, 2, 3, 128
