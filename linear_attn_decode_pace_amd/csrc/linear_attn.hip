@@ -798,19 +798,28 @@ LinearPlan linear_plan(int B, int H, int dk, int dv, int T, int bf16) {
     // (the bf16 kernel's offsets within a chunk have 32 bits)
     LinearPlan p{T > 16 && (double)B * H * std::max(dk, dv) * 64 < 4294967296.0, dv <= 64 ? 1 : 2, 1, 1, T};
     if (!p.chunked) return p;
-    // float32: half the columns a workgroup where units would idle, as its chunks are
-    // bound by a wave's products (128 states of 128 x 128: 256 tokens 40 us against 57,
-    // 2048 tokens 293 against 323; 1024 states 252 against 220, so not there)
-    if (!bf16 && (long long)B * H * ((dv + 127) / 128) < 256) p.ct = 1;
+    const long long states = (long long)B * H, wide = states * ((dv + 127) / 128), chunks = (T + LC - 1) / LC;
+    // a segment reads K and V twice and moves 8 d_k d_v bytes of states, in three launches
+    // instead of one: at least two chunks of it and four of them, and only until two
+    // workgroups a unit are there, or three where the states are half as large
+    // (16 states of 16384 tokens, d_k = 128: 146 us with 512 workgroups, 172 us with 768
+    // and 165 us with 256 when chosen; 84 states of up to 1999 tokens, d_k = 64: 64 us with
+    // 512, 55 us with 768; 16 states of 1024 tokens: 25 us with two chunks, 30 us with four;
+    // 128 states of 256 tokens: 27 us in one segment, 37 us in two)
+    auto segments = [&](long long groups) {
+        const long long want = groups >= 256 ? 1 : (dk == 64 ? 768 : 512) / groups;
+        return chunks < 8 ? 1 : std::min(want, chunks / 2);
+    };
+    // half the columns a workgroup where units would idle otherwise, or where that fills
+    // them in place of a few segments (128 states of 256 tokens: 20 us against 27; of
+    // 1024: 60 against 80; d_k = 64, 225 states of 3316 tokens: 198 us against 285 in three
+    // segments, 176 of 1024 58 against 73 in four, but 176 of up to 4096 207 against 180).
+    // float32: wherever units are not all busy, as its chunks are bound by a wave's
+    // products (128 states of 128 x 128: 2048 tokens 293 us against 323; 1024
+    // states of 256 tokens 252 against 220, so not there)
+    if (wide < 256 && (!bf16 || (wide >= 128 && segments(wide) <= (chunks < 32 ? 4 : 3)) || wide * segments(wide) < 256)) p.ct = 1;
     p.col_blocks = (dv + 64 * p.ct - 1) / (64 * p.ct);
-    const long long groups = (long long)B * H * p.col_blocks, chunks = (T + LC - 1) / LC;
-    // a segment reads K and V twice and moves 8 d_k d_v bytes of states: at least
-    // four chunks of it, and only until two workgroups a unit are there, or three
-    // where the states are half as large (16 states of 16384 tokens, d_k = 128:
-    // 146 us with 512 workgroups, 172 us with 768 and 165 us with 256 when chosen; 84
-    // states of up to 1999 tokens, d_k = 64: 64 us with 512, 55 us with 768)
-    const long long want = groups >= 256 ? 1 : (dk == 64 ? 768 : 512) / groups;
-    const long long segs = std::max(1ll, std::min(want, chunks / 4));
+    const long long segs = segments(states * p.col_blocks);
     p.seg_len = (int)((chunks + segs - 1) / segs) * LC;
     p.segs = (T + p.seg_len - 1) / p.seg_len;
     return p;
