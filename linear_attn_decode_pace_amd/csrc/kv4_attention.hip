@@ -706,9 +706,18 @@ Plan plan_for(const Kv4View &c, int G, int T, int window, int sinks, int bf16) {
     p.row_blocks = (int)((R + rows - 1) / rows);
     const long long groups = heads * p.row_blocks, tiles = tiles_of(rows);
     if (p.wr == 4) {
-        // many rows: their partial results cost more than idle units, so only to
-        // two workgroups a unit
-        p.splits = (int)std::min(512 / groups, tiles / 4);
+        // many rows: their partial results cost more than idle units, so only until all
+        // have a place on the card at once (two a unit, three of 64 channels); from eight
+        // tiles a workgroup on also to the fewest parts that leave at most 15% of the places
+        // empty in the last round (384 workgroups of 256 tiles: 469 us whole, 378 us in
+        // four parts; 320 of 128 tiles: 243 and 188 us)
+        const long long places = c.d == 64 ? 768 : 512;
+        p.splits = (int)std::max(1ll, std::min(places / groups, tiles / 4));
+        for (long long s = p.splits; s <= std::min(tiles / 8, 8ll); ++s)
+            if (groups * s * 100 >= 85 * places * ((groups * s + places - 1) / places)) {
+                p.splits = (int)s;
+                break;
+            }
     } else {
         // few rows: to two workgroups a unit at four tiles a wave, and beyond, as lengths
         // differ, to sixteen at 32 tiles (at four: 64 caches of up to 1024 tokens, 23 us against
@@ -718,6 +727,8 @@ Plan plan_for(const Kv4View &c, int G, int T, int window, int sinks, int bf16) {
                                  std::min((4095 + groups) / groups, tiles / (32 * wk)));
     }
     p.splits = std::max(1, std::min(p.splits, 256));
+    // the workspace is that of a call without a window
+    if (window) p.splits = std::min(p.splits, plan_for(c, G, T, 0, 0, bf16).splits);
     return p;
 }
 
