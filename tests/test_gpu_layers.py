@@ -236,6 +236,17 @@ def test_linear_attention_steps_of_odd_widths(t, b, h, dk, dv, ragged, start, dt
     assert ((state_got - end).abs() <= 2 * t * ref.U32 * 1.001 * end_mass).all()
 
 
+@pytest.mark.parametrize("t,b,h,dk,dv,ragged,start", [
+    (70, 64, 5, 128, 128, True, True),                 # states enough for wide column blocks
+    (37, 43, 6, 64, 240, True, False),
+    (600, 12, 5, 64, 128, True, True),                 # and of segments
+    (520, 3, 21, 128, 128, False, True),
+    (1300, 2, 8, 128, 64, True, False),
+])
+def test_linear_attention_of_many_states(t, b, h, dk, dv, ragged, start):
+    test_linear_attention(t, b, h, dk, dv, BF16, ragged, start)
+
+
 def test_linear_attention_prompt_then_steps():
     """A prompt in two calls, then single tokens, equals one call over all of them."""
     t, b, h, d = 150, 2, 3, 128
@@ -439,6 +450,16 @@ def test_cache_attention(b, hk, group, t, n, d, page, window, sinks, holes, dtyp
     (2, 1, 5, 9, 2100, 256, 96, 333, 1, False),
 ])
 def test_cache_attention_wide_heads_and_long_caches(b, hk, group, t, n, d, page, window, sinks, holes, dtype):
+    test_cache_attention(b, hk, group, t, n, d, page, window, sinks, holes, dtype)
+
+
+@pytest.mark.parametrize("b,hk,group,t,n,d,page,window,sinks,holes,dtype", [
+    (2, 4, 4, 300, 5600, 128, 64, 0, 0, True, BF16),   # long lists of tiles: 32 rows a wave, several parts
+    (2, 4, 4, 1000, 2500, 64, 64, 1500, 40, False, BF16),
+    (1, 2, 8, 260, 2600, 256, 32, 0, 0, True, BF16),
+    (1, 2, 8, 130, 1500, 64, 32, 0, 0, False, F32),
+])
+def test_cache_attention_of_long_blocks(b, hk, group, t, n, d, page, window, sinks, holes, dtype):
     test_cache_attention(b, hk, group, t, n, d, page, window, sinks, holes, dtype)
 
 
