@@ -42,7 +42,6 @@ __device__ inline float wave_sum(float x) {
     return x;
 }
 
-
 // sine and cosine of pos * freq: the product and its reduction to a turn in
 // float64 (within 2^-24 of a turn), the functions in float32
 __device__ inline f32x2 turn(int pos, float freq) {
@@ -248,8 +247,10 @@ bool try_units(const NormArgs &a, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_qk_norm_rope(const NormArgs &a, int bf16, hipStream_t s) {
-    if (bf16 ? try_units<uint16_t, 8>(a, s) || try_units<uint16_t, 2>(a, s)
-             : try_units<float, 4>(a, s) || try_units<float, 1>(a, s))
+    // the widest vectors that the sizes allow (12986 rows of 48 heads of 96 channels, 24 rotated,
+    // bf16: 55 us by four elements, 85 us by two)
+    if (bf16 ? try_units<uint16_t, 8>(a, s) || try_units<uint16_t, 4>(a, s) || try_units<uint16_t, 2>(a, s)
+             : try_units<float, 4>(a, s) || try_units<float, 2>(a, s) || try_units<float, 1>(a, s))
         return hipGetLastError();
     const long long units = a.tokens * a.heads;
     const unsigned blocks = (unsigned)((units + 3) / 4);

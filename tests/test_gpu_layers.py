@@ -78,6 +78,19 @@ def test_norm_rope(tokens, hq, hk, d, norm, rot, adjacent, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("tokens,hq,hk,d,norm,rot,adjacent", [
+    (19, 5, 3, 96, "rms", 24, False),                  # vectors of every width
+    (19, 3, 8, 80, "none", 40, True),
+    (6, 2, 1, 72, "l2", 8, False),
+    (6, 2, 1, 100, "rms", 36, False),
+    (300, 1, 1, 80, "rms", 20, False),
+    (1100, 4, 2, 104, "l2", 56, True),
+])
+def test_norm_rope_widths(tokens, hq, hk, d, norm, rot, adjacent, dtype):
+    test_norm_rope(tokens, hq, hk, d, norm, rot, adjacent, dtype)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("d,rot,adjacent", [(128, 64, False), (80, 20, False), (256, 256, True), (33, 0, False)])
 def test_norm_in_place_and_unaligned_rows(d, rot, adjacent, dtype):
     g = ref.gen(d)
